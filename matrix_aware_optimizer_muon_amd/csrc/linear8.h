@@ -1,0 +1,96 @@
+// Internal launch interface of the 8-bit linear layer's kernels
+// (include/muon_linear8.h): linear8_rows.hip holds the row-wise ones,
+// linear8_gemm.hip the products, linear8_api.cpp validates and dispatches.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace muon {
+namespace l8 {
+
+// Widest row the row-wise kernels hold in registers (16 waves of 64 lanes,
+// 4 chunks of 8 columns each).
+constexpr int64_t kMaxCols = 32768;
+
+struct NormParams {
+  const void* x;
+  const void* res;     // nullptr: no residual
+  const float* w;
+  void* h;             // x + res, written only with a residual
+  void* y;             // normalised rows, or nullptr with q
+  int8_t* q;
+  float* scale;
+  float* rstd;
+  int64_t rows, cols;
+  int64_t ldx, ldr, ldh, ldy, ldq;
+  double eps;
+};
+
+struct NormBackParams {
+  const void* dy;
+  const void* h;       // rows of the planned type, or int8 with hscale
+  const float* hscale;
+  const float* rstd;
+  const float* w;
+  const void* dh;      // nullable
+  void* dx;
+  float* part;         // [groups][cols] sums of dw, or dw itself (1 group)
+  int64_t rows, cols;
+  int64_t lddy, ldh, lddh, lddx;
+  int groups;
+};
+
+// bf16 selects the 16-bit type of every typed row, else fp32.
+hipError_t launch_norm(const NormParams& p, bool bf16, hipStream_t s);
+hipError_t launch_norm_back(const NormBackParams& p, bool bf16, hipStream_t s);
+hipError_t launch_norm_back_sum(const float* part, float* dw, int groups, int64_t cols, hipStream_t s);
+int norm_back_groups(int64_t rows, int64_t cols);
+hipError_t launch_quantize(const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
+                           int64_t rows, int64_t cols, bool bf16, hipStream_t s);
+hipError_t launch_dequantize(const int8_t* q, int64_t ldq, const float* scale, void* x, int64_t ldx,
+                             int64_t rows, int64_t cols, bool bf16, hipStream_t s);
+
+// One operand of a product as the tile kernels read it: `rows` rows of `ld`
+// bytes, 16-byte aligned, ld a multiple of 16.
+//
+// Products: C[q][p] = sum_k P(p, k) Q(q, k), C row-major with the P index
+// contiguous.  An operand is K-contiguous (its rows are p or q) or K-major
+// (its rows are k).
+enum ProductKind {
+  KIND_I8 = 0,      // int8 x int8 -> int32, both K-contiguous
+  KIND_DX = 1,      // bf16, P K-major, Q K-contiguous (input gradient)
+  KIND_DW = 2       // bf16, P and Q K-major (weight gradient)
+};
+
+struct MmParams {
+  const char* P;
+  const char* Q;
+  int64_t ldp, ldq;         // bytes
+  int np, nq, kd;           // output columns, output rows, contraction
+  int tile;                 // 256 or 128
+  int splits;               // contraction ranges (partials in `part` if > 1)
+  const float* sp;          // per output column, per output row (KIND_I8)
+  const float* sq;
+  void* out;                // bf16 or fp32
+  int64_t ldo;              // elements
+  bool obf16, accumulate;
+  float* part;              // [splits][nq][np], int32 bits for KIND_I8
+};
+
+hipError_t launch_mm(const MmParams& p, ProductKind kind, hipStream_t s);
+hipError_t launch_mm_sum(const MmParams& p, ProductKind kind, hipStream_t s);
+
+// The product for at most kFewRows rows of x (one generated token and short
+// batches): no tiles, no alignment, reads the weights once.
+constexpr int kFewRows = 16;
+hipError_t launch_few(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw,
+                      const float* ws, void* y, int64_t ldy, bool bf16, int t, int n, int k, hipStream_t s);
+
+// dst[r][0 .. ld) = src[r][0 .. bytes), zeros beyond; ld a multiple of 16,
+// dst 16-byte aligned, src at any address.
+hipError_t launch_pack(const void* src, int64_t lds, int64_t bytes, void* dst, int64_t ld, int64_t rows,
+                       hipStream_t s);
+
+}  // namespace l8
+}  // namespace muon

@@ -1,0 +1,307 @@
+// C ABI of the 8-bit linear layer (include/muon_linear8.h): validation, the
+// choice of kernel, tile and split, and the launch sequence.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "linear8.h"
+#include "muon_linear8.h"
+
+using namespace muon::l8;
+
+namespace {
+
+constexpr int64_t kMaxDim = 1ll << 24;
+constexpr int64_t kMaxK8 = 131071;  // 128 * 128 * k stays below 2^31
+
+bool known(muon_dtype t) { return t == MUON_F32 || t == MUON_BF16; }
+int64_t size_of(muon_dtype t) { return t == MUON_BF16 ? 2 : 4; }
+bool aligned(const void* p, int64_t a) { return (uintptr_t)p % (uintptr_t)a == 0; }
+int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+muon_status hip(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_ERR_HIP; }
+
+// A matrix argument: present, aligned to its elements, rows that do not
+// overlap.
+bool matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t size) {
+  return p && aligned(p, size) && (rows <= 1 || ld >= cols);
+}
+
+muon_status row_sizes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 1) return MUON_ERR_INVALID_ARGUMENT;
+  if (rows > 0x7fffffff || cols > kMaxCols) return MUON_ERR_UNSUPPORTED;
+  return MUON_OK;
+}
+
+// How a product runs.  `few`: the kernel for at most kFewRows rows of x.
+struct Choice {
+  bool few = false;
+  bool pack_q = false, pack_p = false;
+  int64_t ldq = 0, ldp = 0;        // bytes, as the tile kernel reads them
+  int64_t at_q = 0, at_p = 0, at_part = 0;
+  int tile = 128, splits = 1;
+  int np = 0, nq = 0, kd = 0;
+  int64_t bytes = 0;
+};
+
+Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t t,
+              int64_t n, int64_t k) {
+  Choice c;
+  const bool i8 = kind == MUON_Q8_MATMUL;
+  if (i8 && t <= kFewRows) {
+    c.few = true;
+    return c;
+  }
+  // a is Q, b is P; their stored shapes
+  const int64_t sa = i8 ? 1 : 2;
+  const int64_t a_cols = i8 ? k : n;
+  const int64_t b_rows = kind == MUON_Q8_GRAD_WEIGHT ? t : n, b_cols = k;
+  c.np = (int)(i8 ? n : k);
+  c.nq = (int)(kind == MUON_Q8_GRAD_WEIGHT ? n : t);
+  c.kd = (int)(i8 ? k : kind == MUON_Q8_GRAD_INPUT ? n : t);
+  const int64_t a_rows = t;
+  auto direct = [](const void* p, int64_t ld, int64_t rows, int64_t bytes, int64_t size) {
+    return aligned(p, 16) && bytes % 16 == 0 && (rows <= 1 || ld * size % 16 == 0);
+  };
+  c.pack_q = !direct(a, lda, a_rows, a_cols * sa, sa);
+  c.ldq = c.pack_q ? up(a_cols * sa, 16) : a_rows <= 1 ? a_cols * sa : lda * sa;
+  c.pack_p = !i8 || !direct(b, ldb, b_rows, b_cols, 1);
+  const int64_t sp = i8 ? 1 : 2;
+  c.ldp = c.pack_p ? up(b_cols * sp, 16) : b_rows <= 1 ? b_cols : ldb;
+  if (c.pack_q) {
+    c.at_q = c.bytes;
+    c.bytes += up(a_rows * c.ldq, 256);
+  }
+  if (c.pack_p) {
+    c.at_p = c.bytes;
+    c.bytes += up(b_rows * c.ldp, 256);
+  }
+  auto tiles = [&](int64_t T) { return (int64_t)((c.np + T - 1) / T) * ((c.nq + T - 1) / T); };
+  const int64_t stages = (c.kd + (i8 ? 63 : 31)) / (i8 ? 64 : 32);
+  if (tiles(256) >= 192) {
+    c.tile = 256;
+  } else {
+    c.tile = 128;
+    const int64_t want = 512 / std::max<int64_t>(tiles(128), 1);
+    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, stages / 8, 32}));
+  }
+  if (c.splits > 1) {
+    c.at_part = c.bytes;
+    c.bytes += up((int64_t)c.splits * c.np * c.nq * 4, 256);
+  }
+  return c;
+}
+
+muon_status product_sizes(muon_q8_product kind, int64_t t, int64_t n, int64_t k) {
+  if (t < 0 || n < 0 || k < 0) return MUON_ERR_INVALID_ARGUMENT;
+  if (t > kMaxDim || n > kMaxDim || k > kMaxDim) return MUON_ERR_UNSUPPORTED;
+  if (kind == MUON_Q8_MATMUL && k > kMaxK8) return MUON_ERR_UNSUPPORTED;
+  return MUON_OK;
+}
+
+// Lays the operands out, runs the tiles and joins the splits.
+muon_status run_product(muon_q8_product kind, const void* a, int64_t lda, const float* a_scale,
+                        const int8_t* b, int64_t ldb, const float* b_scale, int64_t t, int64_t n,
+                        int64_t k, void* out, int64_t ldo, muon_dtype dtype, bool accumulate,
+                        void* workspace, size_t workspace_bytes, hipStream_t s) {
+  const muon_status bad = product_sizes(kind, t, n, k);
+  if (bad != MUON_OK) return bad;
+  if (!known(dtype)) return MUON_ERR_INVALID_ARGUMENT;
+  const bool i8 = kind == MUON_Q8_MATMUL;
+  const int64_t a_cols = i8 ? k : n;
+  const int64_t b_rows = kind == MUON_Q8_GRAD_WEIGHT ? t : n;
+  const int64_t o_rows = kind == MUON_Q8_GRAD_WEIGHT ? n : t, o_cols = i8 ? n : k;
+  if (o_rows == 0 || o_cols == 0) return MUON_OK;
+  if (!matrix(out, ldo, o_rows, o_cols, size_of(dtype))) return MUON_ERR_INVALID_ARGUMENT;
+  if (t * a_cols > 0 && !matrix(a, lda, t, a_cols, i8 ? 1 : 2)) return MUON_ERR_INVALID_ARGUMENT;
+  if (b_rows * k > 0 && !matrix(b, ldb, b_rows, k, 1)) return MUON_ERR_INVALID_ARGUMENT;
+  if ((i8 && !a_scale) || (b_rows > 0 && !b_scale)) return MUON_ERR_INVALID_ARGUMENT;
+  const Choice c = choose(kind, a, lda, b, ldb, t, n, k);
+  if (c.bytes > 0) {
+    if (workspace_bytes < (size_t)c.bytes) return MUON_ERR_WORKSPACE_TOO_SMALL;
+    if (!workspace || !aligned(workspace, 256)) return MUON_ERR_INVALID_ARGUMENT;
+  }
+  if (c.few)
+    return hip(launch_few((const int8_t*)a, lda, a_scale, b, ldb, b_scale, out, ldo, dtype == MUON_BF16,
+                          (int)t, (int)n, (int)k, s));
+  char* w = (char*)workspace;
+  MmParams p = {};
+  p.Q = c.pack_q ? w + c.at_q : (const char*)a;
+  p.P = c.pack_p ? w + c.at_p : (const char*)b;
+  p.ldq = c.ldq;
+  p.ldp = c.ldp;
+  p.np = c.np;
+  p.nq = c.nq;
+  p.kd = c.kd;
+  p.tile = c.tile;
+  p.splits = c.splits;
+  p.sq = a_scale;
+  p.sp = b_scale;
+  p.out = out;
+  p.ldo = ldo;
+  p.obf16 = dtype == MUON_BF16;
+  p.accumulate = accumulate;
+  p.part = c.splits > 1 ? (float*)(w + c.at_part) : nullptr;
+  hipError_t e = hipSuccess;
+  if (c.kd > 0) {
+    const int64_t sa = i8 ? 1 : 2;
+    if (c.pack_q) e = launch_pack(a, lda * sa, a_cols * sa, w + c.at_q, c.ldq, t, s);
+    if (e == hipSuccess && c.pack_p)
+      e = i8 ? launch_pack(b, ldb, k, w + c.at_p, c.ldp, b_rows, s)
+             : launch_dequantize(b, ldb, b_scale, w + c.at_p, c.ldp / 2, b_rows, k, true, s);
+  }
+  const ProductKind pk = i8 ? KIND_I8 : kind == MUON_Q8_GRAD_INPUT ? KIND_DX : KIND_DW;
+  if (e == hipSuccess) e = launch_mm(p, pk, s);
+  if (e == hipSuccess && c.splits > 1) e = launch_mm_sum(p, pk, s);
+  return hip(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_rmsnorm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                 const float* weight, muon_dtype dtype, int64_t rows, int64_t cols,
+                                 float eps, void* h, int64_t ldh, void* y, int64_t ldy, int8_t* q,
+                                 int64_t ldq, float* scale, float* rstd, hipStream_t stream) {
+  const muon_status bad = row_sizes(rows, cols);
+  if (bad != MUON_OK) return bad;
+  if (!known(dtype) || !(eps >= 0.0f) || std::isinf(eps)) return MUON_ERR_INVALID_ARGUMENT;
+  if ((y != nullptr) == (q != nullptr) && rows > 0) return MUON_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return MUON_OK;
+  const int64_t sz = size_of(dtype);
+  if (!matrix(x, ldx, rows, cols, sz) || !matrix(weight, cols, 1, cols, 4) || !matrix(rstd, 1, 1, rows, 4))
+    return MUON_ERR_INVALID_ARGUMENT;
+  if (residual && (!matrix(residual, ldr, rows, cols, sz) || !matrix(h, ldh, rows, cols, sz)))
+    return MUON_ERR_INVALID_ARGUMENT;
+  if (y && !matrix(y, ldy, rows, cols, sz)) return MUON_ERR_INVALID_ARGUMENT;
+  if (q && (!matrix(q, ldq, rows, cols, 1) || !matrix(scale, 1, 1, rows, 4))) return MUON_ERR_INVALID_ARGUMENT;
+  NormParams p = {};
+  p.x = x;
+  p.res = residual;
+  p.w = weight;
+  p.h = h;
+  p.y = y;
+  p.q = q;
+  p.scale = scale;
+  p.rstd = rstd;
+  p.rows = rows;
+  p.cols = cols;
+  p.ldx = ldx;
+  p.ldr = ldr;
+  p.ldh = ldh;
+  p.ldy = ldy;
+  p.ldq = ldq;
+  p.eps = (double)eps;
+  return hip(launch_norm(p, dtype == MUON_BF16, stream));
+}
+
+muon_status muon_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t* workspace_bytes) {
+  const muon_status bad = row_sizes(rows, cols);
+  if (bad != MUON_OK) return bad;
+  if (!workspace_bytes) return MUON_ERR_INVALID_ARGUMENT;
+  const int groups = norm_back_groups(rows, cols);
+  *workspace_bytes = groups > 1 ? (size_t)groups * (size_t)cols * 4 : 0;
+  return MUON_OK;
+}
+
+muon_status muon_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh,
+                                  const float* h_scale, const float* rstd, const float* weight,
+                                  const void* dh, int64_t lddh, muon_dtype dtype, int64_t rows,
+                                  int64_t cols, void* dx, int64_t lddx, float* dweight, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream) {
+  size_t need = 0;
+  const muon_status bad = muon_rmsnorm_backward_workspace(rows, cols, &need);
+  if (bad != MUON_OK) return bad;
+  if (!known(dtype) || !matrix(dweight, cols, 1, cols, 4)) return MUON_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return hip(launch_norm_back_sum(nullptr, dweight, 0, cols, stream));  // an empty sum
+  const int64_t sz = size_of(dtype);
+  if (!matrix(dy, lddy, rows, cols, sz) || !matrix(h, ldh, rows, cols, h_scale ? 1 : sz) ||
+      !matrix(dx, lddx, rows, cols, sz) || !matrix(weight, cols, 1, cols, 4) || !matrix(rstd, 1, 1, rows, 4) ||
+      (h_scale && !aligned(h_scale, 4)) || (dh && !matrix(dh, lddh, rows, cols, sz)))
+    return MUON_ERR_INVALID_ARGUMENT;
+  if (need > 0) {
+    if (workspace_bytes < need) return MUON_ERR_WORKSPACE_TOO_SMALL;
+    if (!workspace || !aligned(workspace, 256)) return MUON_ERR_INVALID_ARGUMENT;
+  }
+  NormBackParams p = {};
+  p.dy = dy;
+  p.h = h;
+  p.hscale = h_scale;
+  p.rstd = rstd;
+  p.w = weight;
+  p.dh = dh;
+  p.dx = dx;
+  p.rows = rows;
+  p.cols = cols;
+  p.lddy = lddy;
+  p.ldh = ldh;
+  p.lddh = lddh;
+  p.lddx = lddx;
+  p.groups = norm_back_groups(rows, cols);
+  p.part = p.groups > 1 ? (float*)workspace : dweight;
+  hipError_t e = launch_norm_back(p, dtype == MUON_BF16, stream);
+  if (e == hipSuccess && p.groups > 1) e = launch_norm_back_sum(p.part, dweight, p.groups, cols, stream);
+  return hip(e);
+}
+
+muon_status muon_q8_quantize(const void* x, int64_t ldx, muon_dtype dtype, int64_t rows, int64_t cols,
+                             int8_t* q, int64_t ldq, float* scale, hipStream_t stream) {
+  const muon_status bad = row_sizes(rows, cols);
+  if (bad != MUON_OK) return bad;
+  if (!known(dtype)) return MUON_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return MUON_OK;
+  if (!matrix(x, ldx, rows, cols, size_of(dtype)) || !matrix(q, ldq, rows, cols, 1) ||
+      !matrix(scale, 1, 1, rows, 4))
+    return MUON_ERR_INVALID_ARGUMENT;
+  return hip(launch_quantize(x, ldx, q, ldq, scale, rows, cols, dtype == MUON_BF16, stream));
+}
+
+muon_status muon_q8_dequantize(const int8_t* q, int64_t ldq, const float* scale, int64_t rows,
+                               int64_t cols, void* x, int64_t ldx, muon_dtype dtype,
+                               hipStream_t stream) {
+  const muon_status bad = row_sizes(rows, cols);
+  if (bad != MUON_OK) return bad;
+  if (!known(dtype)) return MUON_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return MUON_OK;
+  if (!matrix(x, ldx, rows, cols, size_of(dtype)) || !matrix(q, ldq, rows, cols, 1) ||
+      !matrix(scale, 1, 1, rows, 4))
+    return MUON_ERR_INVALID_ARGUMENT;
+  return hip(launch_dequantize(q, ldq, scale, x, ldx, rows, cols, dtype == MUON_BF16, stream));
+}
+
+muon_status muon_q8_workspace(muon_q8_product product, const void* a, int64_t lda, const void* b,
+                              int64_t ldb, int64_t t, int64_t n, int64_t k, size_t* workspace_bytes) {
+  if (product < MUON_Q8_MATMUL || product > MUON_Q8_GRAD_WEIGHT || !workspace_bytes)
+    return MUON_ERR_INVALID_ARGUMENT;
+  const muon_status bad = product_sizes(product, t, n, k);
+  if (bad != MUON_OK) return bad;
+  *workspace_bytes = (size_t)choose(product, a, lda, b, ldb, t, n, k).bytes;
+  return MUON_OK;
+}
+
+muon_status muon_q8_matmul(const int8_t* xq, int64_t ldx, const float* x_scale, const int8_t* wq,
+                           int64_t ldw, const float* w_scale, int64_t t, int64_t n, int64_t k, void* y,
+                           int64_t ldy, muon_dtype dtype, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream) {
+  return run_product(MUON_Q8_MATMUL, xq, ldx, x_scale, wq, ldw, w_scale, t, n, k, y, ldy, dtype, false,
+                     workspace, workspace_bytes, stream);
+}
+
+muon_status muon_q8_grad_input(const void* dy, int64_t lddy, const int8_t* wq, int64_t ldw,
+                               const float* w_scale, int64_t t, int64_t n, int64_t k, void* dx,
+                               int64_t lddx, muon_dtype dtype, void* workspace, size_t workspace_bytes,
+                               hipStream_t stream) {
+  return run_product(MUON_Q8_GRAD_INPUT, dy, lddy, nullptr, wq, ldw, w_scale, t, n, k, dx, lddx, dtype,
+                     false, workspace, workspace_bytes, stream);
+}
+
+muon_status muon_q8_grad_weight(const void* dy, int64_t lddy, const int8_t* xq, int64_t ldx,
+                                const float* x_scale, int64_t t, int64_t n, int64_t k, void* dw,
+                                int64_t lddw, muon_dtype dtype, int accumulate, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  return run_product(MUON_Q8_GRAD_WEIGHT, dy, lddy, nullptr, xq, ldx, x_scale, t, n, k, dw, lddw, dtype,
+                     accumulate != 0, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,176 @@
+"""Host-side checks of the 8-bit linear layer's C ABI and torch entry points,
+no GPU needed: exports, refusals before any device memory is touched (the
+pointers here are not device memory), empty calls, and workspace sizes."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+from matrix_aware_optimizer_muon_amd import _lib as L
+from matrix_aware_optimizer_muon_amd import linear8 as l8
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(__file__)), "include", "muon_linear8.h")
+OK, INVALID, UNSUPPORTED, SMALL = 0, 1, 2, 3
+P = 1 << 20  # a non-null, 256-byte aligned address that is never read
+
+
+def test_header_and_binding_agree():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = set(re.findall(r"^\s*(?:const\s+)?\w+\**\s+\**(\w+)\s*\(", text, flags=re.M))
+    assert names == set(l8.EXPORTED)
+    lib = L.load()
+    for n in names:
+        assert hasattr(lib, n)
+
+
+def norm(x=P, ldx=64, res=0, ldr=0, w=P, dtype=1, rows=4, cols=64, eps=1e-6, h=0, ldh=0, y=P, ldy=64,
+         q=0, ldq=0, scale=0, rstd=P):
+    return l8._abi().muon_rmsnorm_forward(x, ldx, res, ldr, w, dtype, rows, cols, eps, h, ldh, y, ldy, q,
+                                          ldq, scale, rstd, None)
+
+
+@pytest.mark.parametrize("kw, want", [
+    ({"cols": 0}, INVALID), ({"rows": -1}, INVALID), ({"cols": 32769, "ldx": 32769, "ldy": 32769}, UNSUPPORTED),
+    ({"rows": 1 << 31}, UNSUPPORTED), ({"dtype": 2}, INVALID), ({"eps": -1.0}, INVALID),
+    ({"eps": float("nan")}, INVALID), ({"eps": float("inf")}, INVALID), ({"x": 0}, INVALID),
+    ({"x": P + 1}, INVALID), ({"dtype": 0, "x": P + 2}, INVALID), ({"ldx": 63}, INVALID), ({"w": 0}, INVALID),
+    ({"rstd": 0}, INVALID), ({"y": 0}, INVALID), ({"q": P, "ldq": 64, "scale": P}, INVALID),
+    ({"y": 0, "q": P, "ldq": 64, "scale": 0}, INVALID), ({"y": 0, "q": P, "ldq": 60, "scale": P}, INVALID),
+    ({"res": P, "ldr": 64}, INVALID), ({"res": P, "ldr": 8, "h": P, "ldh": 64}, INVALID),
+    ({"res": P, "ldr": 64, "h": P, "ldh": 63}, INVALID), ({"rows": 0, "x": 0, "y": 0, "rstd": 0}, OK)])
+def test_norm_refusals(kw, want):
+    assert norm(**kw) == want
+
+
+def back(dy=P, lddy=64, h=P, ldh=64, hs=0, rstd=P, w=P, dh=0, lddh=0, dtype=1, rows=4, cols=64, dx=P,
+         lddx=64, dw=P, ws=P, wsb=1 << 20):
+    return l8._abi().muon_rmsnorm_backward(dy, lddy, h, ldh, hs, rstd, w, dh, lddh, dtype, rows, cols, dx,
+                                           lddx, dw, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw, want", [
+    ({"cols": 0}, INVALID), ({"cols": 40000}, UNSUPPORTED), ({"dtype": -1}, INVALID), ({"dw": 0}, INVALID),
+    ({"dy": 0}, INVALID), ({"h": 0}, INVALID), ({"h": P + 1}, INVALID), ({"hs": P + 2}, INVALID),
+    ({"dx": 0}, INVALID), ({"lddx": 10}, INVALID), ({"dh": P, "lddh": 10}, INVALID), ({"rstd": 0}, INVALID),
+    ({"w": 0}, INVALID), ({"wsb": 1}, SMALL), ({"ws": 0}, INVALID), ({"ws": P + 128}, INVALID)])
+def test_norm_backward_refusals(kw, want):
+    assert back(**kw) == want
+
+
+@pytest.mark.parametrize("kw, want", [
+    ({"rows": 0, "x": 0}, OK), ({"cols": 0}, INVALID), ({"cols": 32769, "ld": 32769}, UNSUPPORTED),
+    ({"dtype": 5}, INVALID), ({"x": 0}, INVALID), ({"x": P + 1}, INVALID), ({"ld": 3}, INVALID),
+    ({"q": 0}, INVALID), ({"ldq": 63}, INVALID), ({"scale": 0}, INVALID), ({"scale": P + 1}, INVALID)])
+def test_quantize_refusals(kw, want):
+    a = dict(x=P, ld=64, dtype=1, rows=4, cols=64, q=P, ldq=64, scale=P)
+    a.update(kw)
+    f = l8._abi()
+    assert f.muon_q8_quantize(a["x"], a["ld"], a["dtype"], a["rows"], a["cols"], a["q"], a["ldq"], a["scale"],
+                              None) == want
+    assert f.muon_q8_dequantize(a["q"], a["ldq"], a["scale"], a["rows"], a["cols"], a["x"], a["ld"],
+                                a["dtype"], None) == want
+
+
+PRODUCTS = ["muon_q8_matmul", "muon_q8_grad_input", "muon_q8_grad_weight"]
+
+
+def product(kind, t=40, n=48, k=64, a=P, lda=None, s=P, b=P, ldb=None, out=P, ldo=None, dtype=0, ws=P,
+            wsb=1 << 30, accumulate=0):
+    f = getattr(l8._abi(), PRODUCTS[kind])
+    lda = lda if lda is not None else (k if kind == 0 else n)
+    ldb = ldb if ldb is not None else k
+    ldo = ldo if ldo is not None else (n if kind == 0 else k)
+    if kind == 0:
+        return f(a, lda, s, b, ldb, s, t, n, k, out, ldo, dtype, ws, wsb, None)
+    if kind == 1:
+        return f(a, lda, b, ldb, s, t, n, k, out, ldo, dtype, ws, wsb, None)
+    return f(a, lda, b, ldb, s, t, n, k, out, ldo, dtype, accumulate, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("kw, want", [
+    ({"t": -1}, INVALID), ({"n": -1}, INVALID), ({"k": -1}, INVALID), ({"t": (1 << 24) + 1}, UNSUPPORTED),
+    ({"dtype": 2}, INVALID), ({"a": 0}, INVALID), ({"b": 0}, INVALID), ({"out": 0}, INVALID),
+    ({"out": P + 2}, INVALID), ({"s": 0}, INVALID), ({"lda": 20}, INVALID), ({"ldb": 20}, INVALID),
+    ({"ldo": 20}, INVALID)])
+def test_product_refusals(kind, kw, want):
+    assert product(kind, **kw) == want
+
+
+def test_product_refusals_by_kind():
+    assert product(0, k=131072) == UNSUPPORTED          # int32 sums
+    assert product(1, a=P + 1) == INVALID               # bf16 dy at an odd address
+    assert product(1, wsb=16) == SMALL and product(2, wsb=16) == SMALL
+    assert product(1, ws=0) == INVALID and product(2, ws=P + 16) == INVALID
+    assert product(0, k=65, wsb=16) == SMALL            # rows that are laid out again
+
+
+def test_products_without_outputs_do_nothing():
+    assert product(0, t=0, a=0, out=0) == OK
+    assert product(0, n=0, b=0, out=0) == OK
+    assert product(1, t=0, a=0, out=0) == OK
+    assert product(1, k=0, b=0, out=0) == OK
+    assert product(2, n=0, a=0, out=0) == OK
+    assert product(2, k=0, b=0, out=0) == OK
+
+
+def ws(kind, t, n, k, a=0, b=0, lda=None, ldb=None):
+    return l8._product_workspace(kind, a, lda or (k if kind == 0 else n), b, ldb or k, t, n, k)
+
+
+def test_workspace_sizes():
+    assert ws(0, 1, 18944, 3584) == 0 and ws(0, 16, 100, 33) == 0    # few rows: none
+    assert ws(0, 4096, 18944, 3584) == 0                             # aligned, enough tiles
+    assert ws(0, 4096, 18944, 3583) >= (4096 + 18944) * 3584         # both operands padded
+    assert ws(0, 4096, 18944, 3584, a=8) >= 4096 * 3584              # x off its 16 bytes
+    assert ws(0, 4096, 18944, 3584, ldb=3600) == 0
+    assert ws(0, 4096, 18944, 3584, ldb=3601) >= 18944 * 3584
+    assert ws(1, 4096, 18944, 3584) >= 18944 * 3584 * 2              # the widened weights
+    assert ws(2, 4096, 18944, 3584) >= 4096 * 3584 * 2               # the widened checkpoint
+    z = ctypes.c_size_t()
+    f = l8._abi().muon_q8_workspace
+    assert f(3, 0, 1, 0, 1, 1, 1, 1, ctypes.addressof(z)) == INVALID
+    assert f(0, 0, 1, 0, 1, 1, 1, 1, None) == INVALID
+    assert f(0, 0, 1, 0, 1, 1, 1, 131072, ctypes.addressof(z)) == UNSUPPORTED
+    assert l8._back_workspace(1, 3584) == 0                          # one group writes dweight itself
+    assert l8._back_workspace(8192, 3584) % (4 * 3584) == 0
+
+
+def test_torch_entry_points_refuse():
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        l8.quantize(x)
+    with pytest.raises(ValueError, match="CUDA"):
+        l8.rmsnorm(x, torch.ones(8))
+    q = l8.Q8(torch.zeros(4, 8, dtype=torch.int8), torch.ones(4))
+    with pytest.raises(ValueError, match="CUDA"):
+        l8.dequantize(q)
+    with pytest.raises(ValueError, match="Q8"):
+        l8.matmul(x, q)
+    with pytest.raises(ValueError, match="last dimension"):
+        l8.matmul(q, l8.Q8(torch.zeros(3, 9, dtype=torch.int8), torch.ones(3)))
+    with pytest.raises(ValueError, match="int8"):
+        l8.matmul(l8.Q8(x, torch.ones(4)), q)
+    with pytest.raises(ValueError, match="scale"):
+        l8.matmul(l8.Q8(q.q, torch.ones(5)), q)
+    with pytest.raises(ValueError, match="bf16"):
+        l8.grad_input(x, q)
+    with pytest.raises(ValueError, match="number of rows"):
+        l8.grad_weight(torch.zeros(5, 8, dtype=torch.bfloat16), q)
+    with pytest.raises(ValueError, match="shape"):
+        l8.rmsnorm_backward(x, torch.zeros(4, 9), torch.ones(4), torch.ones(8))
+
+
+def test_rows_of_tensors():
+    t = torch.zeros(6, 20)
+    assert l8._rows(t[:, :8], "t") == (6, 8, 20)
+    assert l8._rows(t[1:2, 3:8], "t") == (1, 5, 20)
+    assert l8._rows(torch.zeros(2, 3, 4), "t") == (6, 4, 4)
+    assert l8._rows(torch.zeros(5), "t") == (1, 5, 5)
+    assert l8._rows(torch.zeros(0, 7), "t") == (0, 7, 7)
+    assert l8._rows(torch.zeros(2, 3, 0), "t") == (6, 0, 0)
+    for bad in (t.t(), t[:, ::2], t[:1].expand(6, 20), torch.zeros(2, 3, 4).transpose(0, 1), torch.zeros(())):
+        with pytest.raises(ValueError):
+            l8._rows(bad, "t")
