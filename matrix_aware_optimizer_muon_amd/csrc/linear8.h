@@ -51,16 +51,13 @@ hipError_t launch_quantize(const void* x, int64_t ldx, int8_t* q, int64_t ldq, f
 hipError_t launch_dequantize(const int8_t* q, int64_t ldq, const float* scale, void* x, int64_t ldx,
                              int64_t rows, int64_t cols, bool bf16, hipStream_t s);
 
-// One operand of a product as the tile kernels read it: `rows` rows of `ld`
-// bytes, 16-byte aligned, ld a multiple of 16.
-//
 // Products: C[q][p] = sum_k P(p, k) Q(q, k), C row-major with the P index
 // contiguous.  An operand is K-contiguous (its rows are p or q) or K-major
 // (its rows are k).
 enum ProductKind {
   KIND_I8 = 0,      // int8 x int8 -> int32, both K-contiguous
-  KIND_DX = 1,      // bf16, P K-major, Q K-contiguous (input gradient)
-  KIND_DW = 2       // bf16, P and Q K-major (weight gradient)
+  KIND_DX = 1,      // P int8 K-major, Q bf16 K-contiguous (input gradient)
+  KIND_DW = 2       // P int8 K-major, Q bf16 K-major (weight gradient)
 };
 
 struct MmParams {
@@ -69,17 +66,18 @@ struct MmParams {
   int64_t ldp, ldq;         // bytes
   int np, nq, kd;           // output columns, output rows, contraction
   int tile;                 // 256 or 128
-  int splits;               // contraction ranges (partials in `part` if > 1)
-  const float* sp;          // per output column, per output row (KIND_I8)
-  const float* sq;
+  bool unaligned;           // an operand that the DMA would read has rows off 16 bytes (tile 128)
+  int direct;               // tiles of one workgroup; the others are split
+  int splits;               // contraction ranges of a split tile
+  const float* sp;          // KIND_I8: per output column; else per row of P
+  const float* sq;          // KIND_I8: per output row
   void* out;                // bf16 or fp32
   int64_t ldo;              // elements
   bool obf16, accumulate;
-  float* part;              // [splits][nq][np], int32 bits for KIND_I8
+  float* part;              // [split tiles][splits][tile][tile], int32 bits for KIND_I8
 };
 
 hipError_t launch_mm(const MmParams& p, ProductKind kind, hipStream_t s);
-hipError_t launch_mm_sum(const MmParams& p, ProductKind kind, hipStream_t s);
 
 // The product for at most kFewRows rows of x (one generated token and short
 // batches): no tiles, no alignment, reads the weights once.

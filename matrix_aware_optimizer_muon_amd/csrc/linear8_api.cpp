@@ -36,10 +36,11 @@ muon_status row_sizes(int64_t rows, int64_t cols) {
 // How a product runs.  `few`: the kernel for at most kFewRows rows of x.
 struct Choice {
   bool few = false;
+  bool unaligned = false;          // read through registers (tile 128)
   bool pack_q = false, pack_p = false;
   int64_t ldq = 0, ldp = 0;        // bytes, as the tile kernel reads them
   int64_t at_q = 0, at_p = 0, at_part = 0;
-  int tile = 128, splits = 1;
+  int tile = 128, splits = 1, direct = 0;
   int np = 0, nq = 0, kd = 0;
   int64_t bytes = 0;
 };
@@ -54,40 +55,46 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
   }
   // a is Q, b is P; their stored shapes
   const int64_t sa = i8 ? 1 : 2;
-  const int64_t a_cols = i8 ? k : n;
+  const int64_t a_rows = t, a_cols = i8 ? k : n;
   const int64_t b_rows = kind == MUON_Q8_GRAD_WEIGHT ? t : n, b_cols = k;
   c.np = (int)(i8 ? n : k);
   c.nq = (int)(kind == MUON_Q8_GRAD_WEIGHT ? n : t);
   c.kd = (int)(i8 ? k : kind == MUON_Q8_GRAD_INPUT ? n : t);
-  const int64_t a_rows = t;
-  auto direct = [](const void* p, int64_t ld, int64_t rows, int64_t bytes, int64_t size) {
-    return aligned(p, 16) && bytes % 16 == 0 && (rows <= 1 || ld * size % 16 == 0);
-  };
-  c.pack_q = !direct(a, lda, a_rows, a_cols * sa, sa);
-  c.ldq = c.pack_q ? up(a_cols * sa, 16) : a_rows <= 1 ? a_cols * sa : lda * sa;
-  c.pack_p = !i8 || !direct(b, ldb, b_rows, b_cols, 1);
-  const int64_t sp = i8 ? 1 : 2;
-  c.ldp = c.pack_p ? up(b_cols * sp, 16) : b_rows <= 1 ? b_cols : ldb;
-  if (c.pack_q) {
-    c.at_q = c.bytes;
-    c.bytes += up(a_rows * c.ldq, 256);
-  }
-  if (c.pack_p) {
-    c.at_p = c.bytes;
-    c.bytes += up(b_rows * c.ldp, 256);
-  }
+  c.ldq = a_rows <= 1 ? a_cols * sa : lda * sa;
+  c.ldp = b_rows <= 1 ? b_cols : ldb;
+  // what the DMA reads: Q, and P of the integer product
+  const bool off_q = !aligned(a, 16) || c.ldq % 16 || a_cols * sa % 16;
+  const bool off_p = i8 && (!aligned(b, 16) || c.ldp % 16 || b_cols % 16);
   auto tiles = [&](int64_t T) { return (int64_t)((c.np + T - 1) / T) * ((c.nq + T - 1) / T); };
   const int64_t stages = (c.kd + (i8 ? 63 : 31)) / (i8 ? 64 : 32);
-  if (tiles(256) >= 192) {
-    c.tile = 256;
+  c.tile = tiles(256) >= 192 ? 256 : 128;
+  if (c.tile == 256) {
+    c.pack_q = off_q;
+    c.pack_p = off_p;
+    if (c.pack_q) {
+      c.ldq = up(a_cols * sa, 16);
+      c.at_q = c.bytes;
+      c.bytes += up(a_rows * c.ldq, 256);
+    }
+    if (c.pack_p) {
+      c.ldp = up(b_cols, 16);
+      c.at_p = c.bytes;
+      c.bytes += up(b_rows * c.ldp, 256);
+    }
   } else {
-    c.tile = 128;
-    const int64_t want = 512 / std::max<int64_t>(tiles(128), 1);
-    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, stages / 8, 32}));
+    c.unaligned = off_q || off_p;
   }
-  if (c.splits > 1) {
-    c.at_part = c.bytes;
-    c.bytes += up((int64_t)c.splits * c.np * c.nq * 4, 256);
+  // Workgroups that run at once: whole rounds of them take a tile each, the
+  // tiles left over are split along K over one more round.
+  const int64_t slots = c.tile == 256 ? 256 : 512, all = tiles(c.tile), rest = all % slots;
+  c.direct = (int)all;
+  if (rest > 0) {
+    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({slots / rest, stages / 8, 32}));
+    if (c.splits > 1) {
+      c.direct = (int)(all - rest);
+      c.at_part = c.bytes;
+      c.bytes += rest * c.splits * c.tile * c.tile * 4;
+    }
   }
   return c;
 }
@@ -134,6 +141,8 @@ muon_status run_product(muon_q8_product kind, const void* a, int64_t lda, const 
   p.nq = c.nq;
   p.kd = c.kd;
   p.tile = c.tile;
+  p.unaligned = c.unaligned;
+  p.direct = c.direct;
   p.splits = c.splits;
   p.sq = a_scale;
   p.sp = b_scale;
@@ -143,16 +152,13 @@ muon_status run_product(muon_q8_product kind, const void* a, int64_t lda, const 
   p.accumulate = accumulate;
   p.part = c.splits > 1 ? (float*)(w + c.at_part) : nullptr;
   hipError_t e = hipSuccess;
-  if (c.kd > 0) {
+  if (c.pack_q && c.kd > 0) {
     const int64_t sa = i8 ? 1 : 2;
-    if (c.pack_q) e = launch_pack(a, lda * sa, a_cols * sa, w + c.at_q, c.ldq, t, s);
-    if (e == hipSuccess && c.pack_p)
-      e = i8 ? launch_pack(b, ldb, k, w + c.at_p, c.ldp, b_rows, s)
-             : launch_dequantize(b, ldb, b_scale, w + c.at_p, c.ldp / 2, b_rows, k, true, s);
+    e = launch_pack(a, t > 1 ? lda * sa : 0, a_cols * sa, w + c.at_q, c.ldq, t, s);
   }
-  const ProductKind pk = i8 ? KIND_I8 : kind == MUON_Q8_GRAD_INPUT ? KIND_DX : KIND_DW;
-  if (e == hipSuccess) e = launch_mm(p, pk, s);
-  if (e == hipSuccess && c.splits > 1) e = launch_mm_sum(p, pk, s);
+  if (e == hipSuccess && c.pack_p && c.kd > 0) e = launch_pack(b, ldb, k, w + c.at_p, c.ldp, b_rows, s);
+  if (e == hipSuccess)
+    e = launch_mm(p, i8 ? KIND_I8 : kind == MUON_Q8_GRAD_INPUT ? KIND_DX : KIND_DW, s);
   return hip(e);
 }
 

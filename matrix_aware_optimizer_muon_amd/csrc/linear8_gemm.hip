@@ -5,12 +5,12 @@
 // all as C[q][p] = sum_k P(p, k) Q(q, k) with p contiguous in C.  P takes the
 // MFMA's A side, so each lane ends with four consecutive columns of one row.
 //
-// For the gradients P is the 8-bit operand widened to bf16 with its scale
-// folded in (exact for power-of-two scales: an int8 fits bf16's 8 significant
-// bits), so every product of a dY value and a restored one is exact in the
-// fp32 sum.  The widening is a pass of its own: the tile kernel then feeds
-// both operands straight from HBM into LDS, and the pass moves 3 bytes per
-// element of the 8-bit operand, 300 / N of the product's time.
+// For the gradients P is the 8-bit operand, widened to bf16 with its scale
+// folded in on its way from HBM through registers into LDS (exact for
+// power-of-two scales: an int8 fits bf16's 8 significant bits), so every
+// product of a dY value and a restored one is exact in the fp32 sum, and no
+// widened copy exists in memory.  2.5 vector instructions per element, once
+// per workgroup, run between the MFMAs.
 //
 // Tiles: 256 x 256 (8 waves, 2 x 4, each 128 x 64) or 128 x 128 (4 waves,
 // 2 x 2, each 64 x 64).  A stage is 64 bytes of K per operand row (64 int8,
@@ -55,6 +55,14 @@ __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory
 __device__ __forceinline__ int swz_c(int row) { return ((row >> 2) & 1) << 1; }
 __device__ __forceinline__ int swz_k(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) << 1; }
 
+__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
 template <bool I8K> struct Mfma;
 template <> struct Mfma<true> {
   typedef i32x4 Acc;
@@ -69,19 +77,19 @@ template <> struct Mfma<false> {
   }
 };
 
-// Where a lane's DMA instructions read, and how a stage of one operand of T
-// rows (columns, if K-major) is laid out in LDS: 64 bytes per row, or 32 rows
-// of 2 T bytes.
+// One operand of T rows (columns, if K-major) fed by direct global->LDS loads:
+// where a lane's instructions read, stage by stage.  In LDS a stage is 64
+// bytes per row, or 32 rows of 2 T bytes.  Needs 16-byte aligned rows.
 template <bool KM, int T, int NW>
-struct Operand {
-  static constexpr int BYTES = T * KB;
-  static constexpr int NDMA = BYTES / 1024 / NW;  // 1-KB instructions per wave and stage
+struct DmaOperand {
+  static constexpr int NDMA = T * KB / 1024 / NW;  // 1-KB instructions per wave and stage
   const char* src[NDMA];   // stage 0
   const char* tail[NDMA];  // the stage that K's end falls into
   int64_t step;            // bytes from stage to stage
 
   __device__ __forceinline__ void init(const char* base, int64_t ld, int row0, int count, int kd,
-                                       int kbytes, int full, int wave, int lane) {
+                                       int kbytes, int full, int tid) {
+    const int wave = tid >> 6, lane = tid & 63;
     step = KM ? KROWS * ld : (int64_t)KB;
 #pragma unroll
     for (int i = 0; i < NDMA; ++i) {
@@ -105,7 +113,124 @@ struct Operand {
   }
   __device__ __forceinline__ void load(int i, char* stage, int ks, int full, int wave) const {
     const char* s = ks < full ? src[i] + ks * step : tail[i];
-    __builtin_amdgcn_global_load_lds((gbl_ptr_t*)s, (lds_ptr_t*)(stage + (wave * NDMA + i) * 1024), 16, 0, 0);
+    // The compiler puts a wait for every earlier DMA before a read of the LDS
+    // object that the DMA names (the ring's other stages, which are in use).
+    // An address that it cannot follow leaves the waits to this kernel's own
+    // vmcnt count and barrier.
+    uint32_t to = (uint32_t)(uintptr_t)(lds_ptr_t*)(stage + (wave * NDMA + i) * 1024);
+    asm("" : "+s"(to));
+    __builtin_amdgcn_global_load_lds((gbl_ptr_t*)s, (lds_ptr_t*)(uintptr_t)to, 16, 0, 0);
+  }
+};
+
+// The bytes [0, n) of a 16-byte chunk, zeros beyond.
+__device__ __forceinline__ u32x4 load_part(const char* a, int n) {
+  union { u32x4 v; uint8_t e[16]; } b;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) b.e[i] = i < n ? (uint8_t)a[i] : (uint8_t)0;
+  return b.v;
+}
+
+// One operand fed through registers, 16 bytes of a row per lane and chunk:
+// at any address, and, with CONV, int8 rows times their scale widened to
+// bf16 on the way (16 values per lane, two 16-byte LDS writes).  Whole 16-byte
+// reads that leave the row stay inside the matrix for all stages before
+// `safe` (load); load_cut, for any stage, reads what exists, byte by byte
+// where a chunk is cut, and takes zero for the rest.
+template <bool KM, bool CONV, int T, int NT>
+struct RegOperand {
+  static constexpr int CPR = KM ? (CONV ? T / 16 : T / 8) : 4;   // chunks per stage row
+  static constexpr int SROWS = KM ? KROWS : T;                   // stage rows
+  static constexpr int N = SROWS * CPR / NT;                     // chunks per lane
+  static_assert(N * NT == SROWS * CPR && (!CONV || N == 1), "whole chunks per lane");
+  struct Regs {
+    u32x4 v[N];
+    float scale;
+  };
+  const char* src[N];
+  const float* scale;
+  int64_t step;
+  int safe, kd, left;  // left: bytes of the chunk's row from the chunk on
+  int row, col;        // the lane's first stage row, its chunk
+
+  __device__ __forceinline__ void init(const char* base, int64_t ld, const float* sc, int row0, int count,
+                                       int kdim, int kbytes, int full, int tid) {
+    row = tid / CPR;
+    col = tid % CPR;
+    kd = kdim;
+    scale = sc;
+    if constexpr (KM) {
+      constexpr int SZ = CONV ? 1 : 2;
+      const int rb = count * SZ, last = (rb - 1) & ~15;  // row bytes, its last chunk
+      const int c = min(row0 * SZ + col * 16, last);
+      left = rb - c;
+      step = KROWS * ld;
+      // rows whose last chunk, read whole, ends inside the matrix
+      const int over = last + 16 - rb;
+      const int64_t rows = over > 0 ? kd - (over + ld - 1) / ld : kd;
+      safe = rows > 0 ? (int)(rows / KROWS) : 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) src[i] = base + (int64_t)(row + i * (KROWS / N)) * ld + c;
+    } else {
+      step = KB;
+      safe = full;
+      left = kbytes - col * 16;
+#pragma unroll
+      for (int i = 0; i < N; ++i) src[i] = base + (int64_t)min(row0 + row + i * (T / N), count - 1) * ld + col * 16;
+    }
+  }
+  // A stage before `safe`.
+  __device__ __forceinline__ void load(Regs& r, int ks) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) __builtin_memcpy(&r.v[i], src[i] + ks * step, 16);
+    if constexpr (CONV) r.scale = scale[ks * KROWS + row];
+  }
+  // Any stage.
+  __device__ __forceinline__ void load_cut(Regs& r, int ks) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      int n;
+      if constexpr (KM) n = ks * KROWS + row + i * (KROWS / N) < kd ? left : 0;
+      else n = left - ks * KB;
+      r.v[i] = u32x4{0, 0, 0, 0};
+      if (n >= 16) __builtin_memcpy(&r.v[i], src[i] + ks * step, 16);
+      else if (n > 0) r.v[i] = load_part(src[i] + ks * step, n);
+    }
+    if constexpr (CONV) r.scale = ks * KROWS + row < kd ? scale[ks * KROWS + row] : 0.0f;
+  }
+  // Piece q of PIECES of a stage's way into LDS, so that the caller can put
+  // MFMAs between them.
+  static constexpr int PIECES = CONV ? 4 : N;
+  struct Wide {
+    u32x4 lo, hi;
+  };
+  __device__ __forceinline__ void store(const Regs& r, Wide& w, char* stage, int q) const {
+    if constexpr (CONV) {
+      const uint32_t b = r.v[0][q];
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(b >> (8 * e)) * r.scale;
+      const uint32_t d0 = pack_bf16(f[0], f[1]), d1 = pack_bf16(f[2], f[3]);
+      if (q < 2) {
+        w.lo[2 * q] = d0;
+        w.lo[2 * q + 1] = d1;
+      } else {
+        w.hi[2 * q - 4] = d0;
+        w.hi[2 * q - 3] = d1;
+      }
+      if (q == 3) {
+        // swz_k is even, so the lane's two chunks stay side by side
+        char* d = stage + row * (T * 2) + (((2 * col) ^ swz_k(row)) << 4);
+        *(u32x4*)d = w.lo;
+        *(u32x4*)(d + 16) = w.hi;
+      }
+    } else if constexpr (KM) {
+      const int k = row + q * (KROWS / N);
+      *(u32x4*)(stage + k * (T * 2) + ((col ^ swz_k(k)) << 4)) = r.v[q];
+    } else {
+      const int t = row + q * (T / N);
+      *(u32x4*)(stage + t * KB + ((col ^ swz_c(t)) << 4)) = r.v[q];
+    }
   }
 };
 
@@ -138,8 +263,6 @@ struct Reader {
   }
 };
 
-__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
-
 // Four consecutive outputs of one row, n of which exist.
 __device__ __forceinline__ void put4(const MmParams& p, int64_t at, int n, const float v[4]) {
   if (p.obf16) {
@@ -171,49 +294,93 @@ __device__ __forceinline__ void put4(const MmParams& p, int64_t at, int n, const
   }
 }
 
-template <bool I8K, bool PKM, bool QKM, int T>
+template <bool C> struct Cut { static constexpr bool value = C; };
+
+// How the kernel reads its operands: P through registers for the gradients
+// (widened), by DMA or, at unaligned addresses, through registers for the
+// integer product; Q by DMA or, unaligned, through registers.
+template <int KIND, bool UNALIGNED, int T>
 __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_kernel(const MmParams p) {
+  constexpr bool I8K = KIND == KIND_I8, PKM = !I8K, QKM = KIND == KIND_DW;
+  constexpr bool PREG = !I8K || UNALIGNED, QREG = UNALIGNED;
   typedef Mfma<I8K> M;
   typedef typename M::Acc Acc;
   constexpr int NW = T == 256 ? 8 : 4;
   constexpr int WQ = NW / 2;                     // waves along Q (2 along P)
   constexpr int FP = T / 2 / 16, FQ = T / WQ / 16;  // 16 x 16 blocks per wave
   constexpr int H = FP / 2;                      // block rows per half stage
-  typedef Operand<PKM, T, NW> OpP;
-  typedef Operand<QKM, T, NW> OpQ;
-  constexpr int DPS = OpP::NDMA + OpQ::NDMA;
-  constexpr int STAGE = OpP::BYTES + OpQ::BYTES;
-  __shared__ __attribute__((aligned(1024))) char smem[STAGES * STAGE];
+  typedef DmaOperand<PKM, T, NW> DmaP;
+  typedef DmaOperand<QKM, T, NW> DmaQ;
+  typedef RegOperand<PKM, PKM, T, 64 * NW> RegP;
+  typedef RegOperand<QKM, false, T, 64 * NW> RegQ;
+  constexpr int DP = PREG ? 0 : DmaP::NDMA, DPS = DP + (QREG ? 0 : DmaQ::NDMA);
+  constexpr int OPB = T * KB;                    // one operand's stage in LDS
+  constexpr int RS = 2;                          // register sets in flight
+  __shared__ __attribute__((aligned(1024))) char sp_[STAGES * OPB];
+  __shared__ __attribute__((aligned(1024))) char sq_[STAGES * OPB];
 
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wp = wave / WQ, wq = wave % WQ;
   const int q4 = lane >> 4, c16 = lane & 15;
 
+  // The first `direct` tiles belong to one workgroup each, the others to
+  // `splits` workgroups each, a range of K apiece.
   const int tiles_p = (p.np + T - 1) / T, tiles_q = (p.nq + T - 1) / T;
-  const uint32_t bid = xcd_remap_chunked(blockIdx.x, gridDim.x, 32);
-  const int split = bid / (uint32_t)(tiles_p * tiles_q);
+  const int bid = (int)xcd_remap_chunked(blockIdx.x, gridDim.x, 32);
+  int tile = bid, split = 0, splits = 1;
+  const int rest = tiles_p * tiles_q - p.direct;
+  if (bid >= p.direct) {
+    const int u = bid - p.direct;
+    split = u / rest;
+    tile = p.direct + u - split * rest;
+    splits = p.splits;
+  }
   int tp, tq;
-  full_tile_grouped((int)bid - split * tiles_p * tiles_q, tiles_p, tiles_q, 8, &tp, &tq);
+  full_tile_grouped(tile, tiles_p, tiles_q, 8, &tp, &tq);
 
   constexpr int KE = I8K ? 64 : 32;              // K elements per stage
   const int full = p.kd / KE;
   const int nk = (p.kd + KE - 1) / KE;
-  const int k0 = (int)((int64_t)nk * split / p.splits), k1 = (int)((int64_t)nk * (split + 1) / p.splits);
+  const int k0 = (int)((int64_t)nk * split / splits), k1 = (int)((int64_t)nk * (split + 1) / splits);
+  const int kbytes = p.kd * (I8K ? 1 : 2);
 
-  OpP op;
-  OpQ oq;
-  op.init(p.P, p.ldp, tp * T, p.np, p.kd, p.kd * (I8K ? 1 : 2), full, wave, lane);
-  oq.init(p.Q, p.ldq, tq * T, p.nq, p.kd, p.kd * (I8K ? 1 : 2), full, wave, lane);
+  DmaP dp;
+  DmaQ dq;
+  RegP gp;
+  RegQ gq;
+  if constexpr (PREG) gp.init(p.P, p.ldp, p.sp, tp * T, p.np, p.kd, kbytes, full, tid);
+  else dp.init(p.P, p.ldp, tp * T, p.np, p.kd, kbytes, full, tid);
+  if constexpr (QREG) gq.init(p.Q, p.ldq, nullptr, tq * T, p.nq, p.kd, kbytes, full, tid);
+  else dq.init(p.Q, p.ldq, tq * T, p.nq, p.kd, kbytes, full, tid);
   auto dma = [&](int q, int buf, int ks) {
-    char* st = smem + buf * STAGE;
-    if (q < OpP::NDMA) op.load(q, st, ks, full, wave);
-    else oq.load(q - OpP::NDMA, st + OpP::BYTES, ks, full, wave);
+    if (q < DP) dp.load(q, sp_ + buf * OPB, ks, full, wave);
+    else dq.load(q - DP, sq_ + buf * OPB, ks, full, wave);
   };
-  Reader<PKM, T> rp;
-  Reader<QKM, T> rq;
-  rp.init(wp * (T / 2), q4, c16);
-  rq.init(wq * (T / WQ), q4, c16);
+  typename RegP::Regs rp[RS];
+  typename RegQ::Regs rq[RS];
+  typename RegP::Wide wp8;
+  typename RegQ::Wide wq8;
+  auto fetch = [&](auto cut, int set, int ks) {
+    if constexpr (PREG) {
+      if constexpr (decltype(cut)::value) gp.load_cut(rp[set], ks);
+      else gp.load(rp[set], ks);
+    }
+    if constexpr (QREG) {
+      if constexpr (decltype(cut)::value) gq.load_cut(rq[set], ks);
+      else gq.load(rq[set], ks);
+    }
+  };
+  // pieces of a register set's way into LDS
+  constexpr int PP = PREG ? RegP::PIECES : 0, PQ = QREG ? RegQ::PIECES : 0;
+  auto put = [&](int set, int buf, int q) {
+    if (q < PP) gp.store(rp[set], wp8, sp_ + buf * OPB, q);
+    else if (q < PP + PQ) gq.store(rq[set], wq8, sq_ + buf * OPB, q - PP);
+  };
+  Reader<PKM, T> fp;
+  Reader<QKM, T> fq;
+  fp.init(wp * (T / 2), q4, c16);
+  fq.init(wq * (T / WQ), q4, c16);
 
   Acc acc[FP][FQ];
 #pragma unroll
@@ -222,92 +389,135 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
     for (int j = 0; j < FQ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
   u32x4 fa[FP], fb0[FQ], fb1[FQ];
 
-  // A stage's DPS instructions go out in two halves, so that every run of
-  // MFMAs carries the same share: the first half of stage kt + 4 in the second
-  // half of step kt (its buffer is released by that step's barrier), the
-  // rest in the first half of step kt + 1.
+  // DMA: a stage's DPS instructions go out in two halves, so that every run
+  // of MFMAs carries the same share: the first half of stage kt + 4 in the
+  // second half of step kt (its buffer is released by that step's barrier),
+  // the rest in the first half of step kt + 1.
+  // Registers: stage kt + 2 goes into LDS in the second half of step kt, and
+  // its set is loaded again with stage kt + 4, two steps ahead of its use.
 #pragma unroll
   for (int st = 0; st < STAGES; ++st)
 #pragma unroll
     for (int q = 0; q < DPS; ++q)
       if (st < STAGES - 1 || q < DPS / 2) dma(q, st, k0 + st);
-  __builtin_amdgcn_s_waitcnt(wait_imm(2 * DPS + DPS / 2, 15));
+  constexpr int PIECES_ALL = PP + PQ;
+  if constexpr (PIECES_ALL > 0) {
+    // stages 0 .. 3 in flight together; everything has landed before the
+    // loop, so that the waits inside it only count the loop's own loads
+    typename RegP::Regs rp0[2];
+    typename RegQ::Regs rq0[2];
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      if constexpr (PREG) gp.load_cut(rp0[st], k0 + st);
+      if constexpr (QREG) gq.load_cut(rq0[st], k0 + st);
+    }
+#pragma unroll
+    for (int st = 0; st < RS; ++st) fetch(Cut<true>(), st, k0 + 2 + st);
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+#pragma unroll
+      for (int q = 0; q < PP; ++q) gp.store(rp0[st], wp8, sp_ + st * OPB, q);
+#pragma unroll
+      for (int q = 0; q < PQ; ++q) gq.store(rq0[st], wq8, sq_ + st * OPB, q);
+    }
+    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
+  } else {
+    __builtin_amdgcn_s_waitcnt(wait_imm(2 * DPS + DPS / 2, 15));
+  }
   barrier();
 #pragma unroll
-  for (int f = 0; f < H; ++f) fa[f] = rp.get(smem, f);
+  for (int f = 0; f < H; ++f) fa[f] = fp.get(sp_, f);
 #pragma unroll
-  for (int f = 0; f < FQ; ++f) fb0[f] = rq.get(smem + OpP::BYTES, f);
+  for (int f = 0; f < FQ; ++f) fb0[f] = fq.get(sq_, f);
 
-  auto step = [&](int kt, u32x4* fb, u32x4* fbn) {  // kt counts from k0
+  auto step = [&](auto cut, int kt, int set, u32x4* fb, u32x4* fbn) {  // kt counts from k0, set = kt % 2
     const int buf = kt & (STAGES - 1);
-    const char* sb = smem + buf * STAGE;
+    const char* sb = sp_ + buf * OPB;
 #pragma unroll
     for (int j = 0; j < FQ; ++j) M::go(fa[0], fb[j], acc[0][j]);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int f = H; f < FP; ++f) fa[f] = rp.get(sb, f);
+    for (int f = H; f < FP; ++f) fa[f] = fp.get(sb, f);
     __builtin_amdgcn_sched_barrier(0);
-    constexpr int N1 = (H - 1) * FQ, G1 = N1 / (DPS / 2);
+    constexpr int N1 = (H - 1) * FQ, D1 = DPS / 2, G1 = N1 / (D1 > 0 ? D1 : 1);
 #pragma unroll
     for (int n = 0; n < N1; ++n) {
       M::go(fa[1 + n / FQ], fb[n % FQ], acc[1 + n / FQ][n % FQ]);
-      if (n % G1 == G1 - 1) {
-        dma(DPS / 2 + n / G1, (kt + STAGES - 1) & (STAGES - 1), k0 + kt + STAGES - 1);
+      if (D1 > 0 && n % G1 == G1 - 1 && n / G1 < D1) {
+        dma(D1 + n / G1, (kt + STAGES - 1) & (STAGES - 1), k0 + kt + STAGES - 1);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    // stage kt + 1 has landed for this wave (2 DPS later ones may fly) and its
-    // reads of stage kt are done
-    __builtin_amdgcn_s_waitcnt(wait_imm(2 * DPS, 0));
+    // This wave's DMAs of stage kt + 1 have landed (2 DPS later ones may fly;
+    // register loads among them make the wait stricter: counting them in
+    // measured 2-4 % slower on the weight gradients), its LDS writes of stage
+    // kt + 1 and its reads of stage kt are done.
+    __builtin_amdgcn_s_waitcnt(wait_imm(DPS > 0 ? 2 * DPS : 63, 0));
     barrier();
-    const char* sn = smem + ((kt + 1) & (STAGES - 1)) * STAGE;
+    const int nb = ((kt + 1) & (STAGES - 1)) * OPB;
 #pragma unroll
-    for (int f = 0; f < H; ++f) fa[f] = rp.get(sn, f);
+    for (int f = 0; f < H; ++f) fa[f] = fp.get(sp_ + nb, f);
 #pragma unroll
-    for (int f = 0; f < FQ; ++f) fbn[f] = rq.get(sn + OpP::BYTES, f);
+    for (int f = 0; f < FQ; ++f) fbn[f] = fq.get(sq_ + nb, f);
     __builtin_amdgcn_sched_barrier(0);
-    constexpr int N2 = H * FQ, G2 = N2 / (DPS / 2);
+    constexpr int N2 = H * FQ, G2 = N2 / (D1 > 0 ? D1 : 1);
+    constexpr int PIECES = PIECES_ALL, GP = PIECES > 0 ? N2 / (PIECES + 1) : N2;
 #pragma unroll
     for (int n = 0; n < N2; ++n) {
       M::go(fa[H + n / FQ], fb[n % FQ], acc[H + n / FQ][n % FQ]);
-      if (n % G2 == G2 - 1) dma(n / G2, buf, k0 + kt + STAGES);
+      if (D1 > 0 && n % G2 == G2 - 1 && n / G2 < D1) dma(n / G2, buf, k0 + kt + STAGES);
+      if (PIECES > 0 && n % GP == GP - 1 && n / GP < PIECES) put(set, (kt + 2) & (STAGES - 1), n / GP);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (PIECES > 0) {
+      fetch(cut, set, k0 + kt + 2 + RS);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   const int steps = k1 - k0;
+  // Two steps per trip: the Q fragments and the register sets alternate
+  // without copies.  The trips whose register loads stay before the cut
+  // stages come first and carry no checks.
   int kt = 0;
-  for (; kt + 1 < steps; kt += 2) {
-    step(kt, fb0, fb1);
-    step(kt + 1, fb1, fb0);
+  if constexpr (PIECES_ALL > 0) {
+    int safe = steps;
+    if constexpr (PREG) safe = min(safe, gp.safe - k0 - RS - 2);
+    if constexpr (QREG) safe = min(safe, gq.safe - k0 - RS - 2);
+    for (; kt + 1 < safe; kt += 2) {
+      step(Cut<false>(), kt, 0, fb0, fb1);
+      step(Cut<false>(), kt + 1, 1, fb1, fb0);
+    }
   }
-  if (kt < steps) step(kt, fb0, fb1);
+  for (; kt + 1 < steps; kt += 2) {
+    step(Cut<true>(), kt, 0, fb0, fb1);
+    step(Cut<true>(), kt + 1, 1, fb1, fb0);
+  }
+  if (kt < steps) step(Cut<true>(), kt, 0, fb0, fb1);
   __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));  // no load may land after the workgroup's LDS is given back
 
   // acc[i][j][e] is column col0 + 16 i + 4 q4 + e of row row0 + 16 j + c16
-  const int col0 = tp * T + wp * (T / 2) + 4 * q4, row0 = tq * T + wq * (T / WQ) + c16;
+  const int colt = wp * (T / 2) + 4 * q4, rowt = wq * (T / WQ) + c16;
+  if (splits > 1) {  // the raw sums, tile by tile
+    float* part = p.part + ((int64_t)(tile - p.direct) * splits + split) * (T * T);
+#pragma unroll
+    for (int j = 0; j < FQ; ++j)
+#pragma unroll
+      for (int i = 0; i < FP; ++i) *(Acc*)(part + (rowt + 16 * j) * T + colt + 16 * i) = acc[i][j];
+    return;
+  }
+  const int col0 = tp * T + colt, row0 = tq * T + rowt;
 #pragma unroll
   for (int j = 0; j < FQ; ++j) {
     const int r = row0 + 16 * j;
     if (r >= p.nq) continue;
     float sq = 1.0f;
-    if (I8K && p.splits == 1) sq = p.sq[r];
+    if (I8K) sq = p.sq[r];
 #pragma unroll
     for (int i = 0; i < FP; ++i) {
       const int c = col0 + 16 * i;
       const int n = p.np - c;
       if (n <= 0) continue;
-      if (p.splits > 1) {
-        float* dst = p.part + ((int64_t)split * p.nq + r) * p.np + c;
-        if (n >= 4) {
-          __builtin_memcpy(dst, &acc[i][j], 16);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 3; ++e)
-            if (e < n) __builtin_memcpy(dst + e, (const char*)&acc[i][j] + 4 * e, 4);
-        }
-        continue;
-      }
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -319,36 +529,28 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
   }
 }
 
-// C = the splits' partial sums added in order, with the epilogue's scales.
-template <bool I8K>
+// C = the splits' partial sums added in order, with the epilogue's scales:
+// blockIdx.y a split tile, four columns of a row per thread.
+template <bool I8K, int T>
 __global__ void __launch_bounds__(256) mm_sum_kernel(const MmParams p) {
-  const int per = (p.np + 3) / 4;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = id / per;
-  if (r >= p.nq) return;
-  const int c = (int)(id - r * per) * 4, n = min(4, p.np - c);
-  const int64_t plane = (int64_t)p.nq * p.np;
-  const float* src = p.part + r * p.np + c;
+  const int at = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4;
+  const int tiles_p = (p.np + T - 1) / T, tiles_q = (p.nq + T - 1) / T;
+  int tp, tq;
+  full_tile_grouped(p.direct + (int)blockIdx.y, tiles_p, tiles_q, 8, &tp, &tq);
+  const int r = tq * T + at / T, c = tp * T + at % T, n = p.np - c;
+  if (r >= p.nq || n <= 0) return;
   typedef typename Mfma<I8K>::Acc Acc;
-  Acc a = Acc{0, 0, 0, 0};
-  for (int s = 0; s < p.splits; ++s) {
-    Acc b = Acc{0, 0, 0, 0};
-    if (n == 4) {
-      __builtin_memcpy(&b, src + s * plane, 16);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 3; ++e)
-        if (e < n) __builtin_memcpy((char*)&b + 4 * e, src + s * plane + e, 4);
-    }
-    a += b;
-  }
+  const float* src = p.part + (int64_t)blockIdx.y * p.splits * (T * T) + at;
+  Acc a = *(const Acc*)src;
+#pragma unroll 4
+  for (int s = 1; s < p.splits; ++s) a += *(const Acc*)(src + (int64_t)s * (T * T));
   float v[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     v[e] = (float)a[e];
     if constexpr (I8K) v[e] = v[e] * p.sq[r] * p.sp[min(c + e, p.np - 1)];
   }
-  put4(p, r * p.ldo + c, n, v);
+  put4(p, (int64_t)r * p.ldo + c, n, v);
 }
 
 // At most 16 rows of x.  A workgroup takes 16 rows of w; its four waves take
@@ -421,15 +623,22 @@ __global__ void __launch_bounds__(256) pack_kernel(const char* src, int64_t lds,
   }
 }
 
-template <bool I8K, bool PKM, bool QKM>
+template <int KIND>
 hipError_t go_mm(const MmParams& p, hipStream_t s) {
   const int T = p.tile;
-  const int64_t blocks = (int64_t)((p.np + T - 1) / T) * ((p.nq + T - 1) / T) * p.splits;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  if (T == 256)
-    hipLaunchKernelGGL((mm_kernel<I8K, PKM, QKM, 256>), dim3((uint32_t)blocks), dim3(512), 0, s, p);
-  else
-    hipLaunchKernelGGL((mm_kernel<I8K, PKM, QKM, 128>), dim3((uint32_t)blocks), dim3(256), 0, s, p);
+  const int64_t tiles = (int64_t)((p.np + T - 1) / T) * ((p.nq + T - 1) / T), rest = tiles - p.direct;
+  const int64_t blocks = p.direct + rest * p.splits;
+  if (blocks > 0x7fffffff || rest < 0 || (T == 256 && p.unaligned)) return hipErrorInvalidValue;
+  const dim3 grid((uint32_t)blocks);
+  if (T == 256) hipLaunchKernelGGL((mm_kernel<KIND, false, 256>), grid, dim3(512), 0, s, p);
+  else if (p.unaligned) hipLaunchKernelGGL((mm_kernel<KIND, true, 128>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((mm_kernel<KIND, false, 128>), grid, dim3(256), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const dim3 sums((uint32_t)(T * T / 1024), (uint32_t)rest);
+  constexpr bool I8K = KIND == KIND_I8;
+  if (T == 256) hipLaunchKernelGGL((mm_sum_kernel<I8K, 256>), sums, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((mm_sum_kernel<I8K, 128>), sums, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -437,19 +646,11 @@ hipError_t go_mm(const MmParams& p, hipStream_t s) {
 
 hipError_t launch_mm(const MmParams& p, ProductKind kind, hipStream_t s) {
   switch (kind) {
-    case KIND_I8: return go_mm<true, false, false>(p, s);
-    case KIND_DX: return go_mm<false, true, false>(p, s);
-    case KIND_DW: return go_mm<false, true, true>(p, s);
+    case KIND_I8: return go_mm<KIND_I8>(p, s);
+    case KIND_DX: return go_mm<KIND_DX>(p, s);
+    case KIND_DW: return go_mm<KIND_DW>(p, s);
   }
   return hipErrorInvalidValue;
-}
-
-hipError_t launch_mm_sum(const MmParams& p, ProductKind kind, hipStream_t s) {
-  const int64_t threads = (int64_t)((p.np + 3) / 4) * p.nq;
-  const dim3 grid((uint32_t)((threads + 255) / 256));
-  if (kind == KIND_I8) hipLaunchKernelGGL(mm_sum_kernel<true>, grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL(mm_sum_kernel<false>, grid, dim3(256), 0, s, p);
-  return hipGetLastError();
 }
 
 hipError_t launch_few(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw,

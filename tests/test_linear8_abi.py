@@ -102,9 +102,17 @@ def test_product_refusals(kind, kw, want):
 def test_product_refusals_by_kind():
     assert product(0, k=131072) == UNSUPPORTED          # int32 sums
     assert product(1, a=P + 1) == INVALID               # bf16 dy at an odd address
-    assert product(1, wsb=16) == SMALL and product(2, wsb=16) == SMALL
-    assert product(1, ws=0) == INVALID and product(2, ws=P + 16) == INVALID
-    assert product(0, k=65, wsb=16) == SMALL            # rows that are laid out again
+    long = {"t": 4096, "n": 512, "k": 512}              # few tiles: split along K, partial sums
+    for kind in (0, 1, 2):
+        kw = dict(long, k=8192) if kind == 0 else dict(long, n=8192) if kind == 1 else long
+        if kind == 0:
+            kw.update(t=512)
+        if kind == 1:
+            kw.update(t=512)
+        assert product(kind, wsb=16, **kw) == SMALL
+        assert product(kind, ws=0, **kw) == INVALID
+        assert product(kind, ws=P + 16, **kw) == INVALID
+    assert product(0, t=4096, n=4096, k=65, wsb=16) == SMALL  # rows that are laid out again
 
 
 def test_products_without_outputs_do_nothing():
@@ -122,13 +130,14 @@ def ws(kind, t, n, k, a=0, b=0, lda=None, ldb=None):
 
 def test_workspace_sizes():
     assert ws(0, 1, 18944, 3584) == 0 and ws(0, 16, 100, 33) == 0    # few rows: none
-    assert ws(0, 4096, 18944, 3584) == 0                             # aligned, enough tiles
-    assert ws(0, 4096, 18944, 3583) >= (4096 + 18944) * 3584         # both operands padded
-    assert ws(0, 4096, 18944, 3584, a=8) >= 4096 * 3584              # x off its 16 bytes
-    assert ws(0, 4096, 18944, 3584, ldb=3600) == 0
-    assert ws(0, 4096, 18944, 3584, ldb=3601) >= 18944 * 3584
-    assert ws(1, 4096, 18944, 3584) >= 18944 * 3584 * 2              # the widened weights
-    assert ws(2, 4096, 18944, 3584) >= 4096 * 3584 * 2               # the widened checkpoint
+    assert ws(0, 4096, 16384, 3584) == 0                             # aligned, whole rounds of tiles
+    assert ws(0, 4096, 16384, 3583) >= (4096 + 16384) * 3584         # both operands padded
+    assert ws(0, 4096, 16384, 3584, a=8) >= 4096 * 3584              # x off its 16 bytes
+    assert ws(0, 4096, 16384, 3584, ldb=3600) == 0
+    assert ws(0, 4096, 16384, 3584, ldb=3601) >= 16384 * 3584
+    assert ws(1, 4096, 8192, 4096) == 0 and ws(2, 256, 4096, 4096) == 0  # 8-bit rows are read as they are
+    assert ws(1, 4096, 8193, 4096) >= 4096 * 8200 * 2                # dy off its 16 bytes
+    assert ws(2, 8192, 512, 3584) % (128 * 128 * 4) == 0 and ws(2, 8192, 512, 3584) > 0
     z = ctypes.c_size_t()
     f = l8._abi().muon_q8_workspace
     assert f(3, 0, 1, 0, 1, 1, 1, 1, ctypes.addressof(z)) == INVALID
