@@ -1,8 +1,10 @@
-"""Compile libmuon.so (HIP for gfx950) in place, next to this file.
+"""Compile libmuon.so (HIP for gfx950) and _linear8.so (the Python binding of
+the 8-bit linear layer, host code only) in place, next to this file.
 
 Each source is compiled to an object in parallel with hipcc, then linked
 into one shared library.  Packed-fp32 instructions are disabled for all
-device code."""
+device code.  _linear8.so is compiled by the host compiler against torch's
+headers and linked to libmuon.so beside it."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmuon.so")
 SOURCES = ["gemm.hip", "gemm_dma.hip", "rr_fused.hip", "direct_fused.hip", "elementwise.hip", "muon_api.cpp",
            "linear8_rows.hip", "linear8_gemm.hip", "linear8_api.cpp"]
+BINDING = os.path.join(PKG, "_linear8.so")
+BINDING_SOURCE = "linear8_torch.cpp"
 ARCH = os.environ.get("MUON_OFFLOAD_ARCH", "gfx950")
 
 
@@ -32,6 +37,35 @@ def _flags() -> list[str]:
     return ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-I", INCLUDE, "-I", CSRC, "-Wall", "-Wno-unused-function"]
+
+
+def _host_cxx() -> str:
+    for cand in (os.environ.get("CXX"), shutil.which("g++"), shutil.which("c++")):
+        if cand:
+            return cand
+    raise RuntimeError("no host C++ compiler found")
+
+
+def build_binding(verbose: bool = False) -> str:
+    """_linear8.so; needs libmuon.so."""
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(_hipcc())))
+    tmp = BINDING + ".tmp"
+    cmd = [_host_cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-I", inc,
+           "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(rocm, "include"),
+           os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L", lib, "-L", PKG, "-lmuon", "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{BINDING_SOURCE} failed:\n{r.stdout}\n{r.stderr}")
+    if verbose and r.stderr.strip():
+        print(r.stderr, file=sys.stderr)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(verbose: bool = False) -> str:
@@ -58,6 +92,7 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_binding(verbose)
     return LIB
 
 

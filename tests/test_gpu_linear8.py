@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from matrix_aware_optimizer_muon_amd import linear8 as l8
+from linear8_common import GRAD_INPUT, GRAD_WEIGHT, MATMUL, abi, product
 
 pytestmark = pytest.mark.gpu
 
@@ -162,7 +163,7 @@ def test_norm_writes_only_its_rows():
     rows, cols, ld = 9, 515, 530
     x = rand((rows, cols), 1, BF)
     w = rand((cols,), 2)
-    f = l8._abi()
+    f = abi()
     s = torch.cuda.current_stream().cuda_stream
     y = torch.full((rows + 2, ld), GUARD, dtype=BF, device="cuda")
     h = torch.full((rows + 2, ld), GUARD, dtype=BF, device="cuda")
@@ -282,8 +283,7 @@ def check_matmul(t, n, k, dtype, x=None, w=None, scales="pow2"):
     x = x if x is not None else q8rand(t, k, 1, scales)
     w = w if w is not None else q8rand(n, k, 2, scales)
     big, out = guarded(t, n, dtype)
-    l8._product(l8.MATMUL, "matmul", x.q, l8._rows(x.q, "x")[2], x.scale, w.q, l8._rows(w.q, "w")[2], w.scale,
-                t, n, k, out, out.stride(0), l8._typed(out, "out"), False)
+    product(MATMUL, x.q, x.scale, w.q, w.scale, out)
     ref = dense(x) @ dense(w).t().contiguous()
     within(out, ref, ref.abs() * (3 * U * 1.001 + (HALF[BF] * 1.001 if dtype == BF else 0)) + 1e-30, "y")
     check_guard(big, n)
@@ -342,20 +342,19 @@ def test_matmul_empty_and_non_finite_rows():
 
 def check_grad(kind, t, n, k, dtype, dy=None, other=None, scales="pow2", accumulate=False):
     dy = dy if dy is not None else rand((t, n), 5, BF, 1e-2)
-    rows = n if kind == l8.GRAD_INPUT else t
+    rows = n if kind == GRAD_INPUT else t
     other = other if other is not None else q8rand(rows, k, 6, scales)
-    orow = t if kind == l8.GRAD_INPUT else n
+    orow = t if kind == GRAD_INPUT else n
     big, out = guarded(orow, k, dtype)
     base = torch.zeros(orow, k, dtype=torch.float64, device="cuda")
     if accumulate:
         out.copy_(rand((orow, k), 9, dtype))
         base = out.double()
-    ref0 = (dy.double() if kind == l8.GRAD_INPUT else dy.double().t().contiguous())
-    l8._product(kind, "grad", dy, l8._rows(dy, "dy")[2], None, other.q, l8._rows(other.q, "b")[2], other.scale,
-                t, n, k, out, out.stride(0), l8._typed(out, "out"), accumulate)
+    ref0 = (dy.double() if kind == GRAD_INPUT else dy.double().t().contiguous())
+    product(kind, dy, None, other.q, other.scale, out, accumulate)
     ref = ref0 @ dense(other)
     mag = ref0.abs() @ dense(other).abs()
-    kd = n if kind == l8.GRAD_INPUT else t
+    kd = n if kind == GRAD_INPUT else t
     # products are exact for power-of-two scales; every fp32 addition may be
     # off by a whole step (2^-23) of a partial sum
     bound = (kd + 40) * 2 * U * mag + 1e-30
@@ -374,16 +373,16 @@ GRADS = [(1, 1, 1), (1, 300, 7), (7, 33, 64), (32, 32, 128), (33, 31, 129), (64,
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("t, n, k", GRADS)
-@pytest.mark.parametrize("kind", [l8.GRAD_INPUT, l8.GRAD_WEIGHT])
+@pytest.mark.parametrize("kind", [GRAD_INPUT, GRAD_WEIGHT])
 def test_gradient_products(kind, t, n, k, dtype):
     check_grad(kind, t, n, k, dtype)
 
 
-@pytest.mark.parametrize("kind", [l8.GRAD_INPUT, l8.GRAD_WEIGHT])
+@pytest.mark.parametrize("kind", [GRAD_INPUT, GRAD_WEIGHT])
 def test_gradient_products_scales_and_strides(kind):
     t, n, k = 90, 72, 80
     check_grad(kind, t, n, k, F32, scales="any")
-    dy, o = rand((t, n), 5, BF), q8rand(n if kind == l8.GRAD_INPUT else t, k, 6)
+    dy, o = rand((t, n), 5, BF), q8rand(n if kind == GRAD_INPUT else t, k, 6)
     a = check_grad(kind, t, n, k, F32, dy=dy, other=o).clone()
     for off, extra in ((0, 8), (8, 0), (1, 2)):
         b = check_grad(kind, t, n, k, F32, dy=strided(dy, off, extra),
@@ -394,7 +393,7 @@ def test_gradient_products_scales_and_strides(kind):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("t, n, k", [(50, 70, 33), (1500, 130, 264), (0, 20, 30), (40, 3500, 4000)])
 def test_weight_gradient_accumulates(t, n, k, dtype):
-    check_grad(l8.GRAD_WEIGHT, t, n, k, dtype, accumulate=True)
+    check_grad(GRAD_WEIGHT, t, n, k, dtype, accumulate=True)
 
 
 def test_gradient_products_empty():

@@ -10,6 +10,7 @@ import torch
 
 from matrix_aware_optimizer_muon_amd import _lib as L
 from matrix_aware_optimizer_muon_amd import linear8 as l8
+from linear8_common import EXPORTED, abi, back_workspace, workspace
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(__file__)), "include", "muon_linear8.h")
 OK, INVALID, UNSUPPORTED, SMALL = 0, 1, 2, 3
@@ -19,7 +20,7 @@ P = 1 << 20  # a non-null, 256-byte aligned address that is never read
 def test_header_and_binding_agree():
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = set(re.findall(r"^\s*(?:const\s+)?\w+\**\s+\**(\w+)\s*\(", text, flags=re.M))
-    assert names == set(l8.EXPORTED)
+    assert names == set(EXPORTED)
     lib = L.load()
     for n in names:
         assert hasattr(lib, n)
@@ -27,7 +28,7 @@ def test_header_and_binding_agree():
 
 def norm(x=P, ldx=64, res=0, ldr=0, w=P, dtype=1, rows=4, cols=64, eps=1e-6, h=0, ldh=0, y=P, ldy=64,
          q=0, ldq=0, scale=0, rstd=P):
-    return l8._abi().muon_rmsnorm_forward(x, ldx, res, ldr, w, dtype, rows, cols, eps, h, ldh, y, ldy, q,
+    return abi().muon_rmsnorm_forward(x, ldx, res, ldr, w, dtype, rows, cols, eps, h, ldh, y, ldy, q,
                                           ldq, scale, rstd, None)
 
 
@@ -46,7 +47,7 @@ def test_norm_refusals(kw, want):
 
 def back(dy=P, lddy=64, h=P, ldh=64, hs=0, rstd=P, w=P, dh=0, lddh=0, dtype=1, rows=4, cols=64, dx=P,
          lddx=64, dw=P, ws=P, wsb=1 << 20):
-    return l8._abi().muon_rmsnorm_backward(dy, lddy, h, ldh, hs, rstd, w, dh, lddh, dtype, rows, cols, dx,
+    return abi().muon_rmsnorm_backward(dy, lddy, h, ldh, hs, rstd, w, dh, lddh, dtype, rows, cols, dx,
                                            lddx, dw, ws, wsb, None)
 
 
@@ -66,7 +67,7 @@ def test_norm_backward_refusals(kw, want):
 def test_quantize_refusals(kw, want):
     a = dict(x=P, ld=64, dtype=1, rows=4, cols=64, q=P, ldq=64, scale=P)
     a.update(kw)
-    f = l8._abi()
+    f = abi()
     assert f.muon_q8_quantize(a["x"], a["ld"], a["dtype"], a["rows"], a["cols"], a["q"], a["ldq"], a["scale"],
                               None) == want
     assert f.muon_q8_dequantize(a["q"], a["ldq"], a["scale"], a["rows"], a["cols"], a["x"], a["ld"],
@@ -78,7 +79,7 @@ PRODUCTS = ["muon_q8_matmul", "muon_q8_grad_input", "muon_q8_grad_weight"]
 
 def product(kind, t=40, n=48, k=64, a=P, lda=None, s=P, b=P, ldb=None, out=P, ldo=None, dtype=0, ws=P,
             wsb=1 << 30, accumulate=0):
-    f = getattr(l8._abi(), PRODUCTS[kind])
+    f = getattr(abi(), PRODUCTS[kind])
     lda = lda if lda is not None else (k if kind == 0 else n)
     ldb = ldb if ldb is not None else k
     ldo = ldo if ldo is not None else (n if kind == 0 else k)
@@ -125,7 +126,7 @@ def test_products_without_outputs_do_nothing():
 
 
 def ws(kind, t, n, k, a=0, b=0, lda=None, ldb=None):
-    return l8._product_workspace(kind, a, lda or (k if kind == 0 else n), b, ldb or k, t, n, k)
+    return workspace(kind, a, lda or (k if kind == 0 else n), b, ldb or k, t, n, k)
 
 
 def test_workspace_sizes():
@@ -139,12 +140,12 @@ def test_workspace_sizes():
     assert ws(1, 4096, 8193, 4096) >= 4096 * 8200 * 2                # dy off its 16 bytes
     assert ws(2, 8192, 512, 3584) % (128 * 128 * 4) == 0 and ws(2, 8192, 512, 3584) > 0
     z = ctypes.c_size_t()
-    f = l8._abi().muon_q8_workspace
+    f = abi().muon_q8_workspace
     assert f(3, 0, 1, 0, 1, 1, 1, 1, ctypes.addressof(z)) == INVALID
     assert f(0, 0, 1, 0, 1, 1, 1, 1, None) == INVALID
     assert f(0, 0, 1, 0, 1, 1, 1, 131072, ctypes.addressof(z)) == UNSUPPORTED
-    assert l8._back_workspace(1, 3584) == 0                          # one group writes dweight itself
-    assert l8._back_workspace(8192, 3584) % (4 * 3584) == 0
+    assert back_workspace(1, 3584) == 0                          # one group writes dweight itself
+    assert back_workspace(8192, 3584) % (4 * 3584) == 0
 
 
 def test_torch_entry_points_refuse():
@@ -172,14 +173,28 @@ def test_torch_entry_points_refuse():
         l8.rmsnorm_backward(x, torch.zeros(4, 9), torch.ones(4), torch.ones(8))
 
 
-def test_rows_of_tensors():
+def test_row_distances():
     t = torch.zeros(6, 20)
-    assert l8._rows(t[:, :8], "t") == (6, 8, 20)
-    assert l8._rows(t[1:2, 3:8], "t") == (1, 5, 20)
-    assert l8._rows(torch.zeros(2, 3, 4), "t") == (6, 4, 4)
-    assert l8._rows(torch.zeros(5), "t") == (1, 5, 5)
-    assert l8._rows(torch.zeros(0, 7), "t") == (0, 7, 7)
-    assert l8._rows(torch.zeros(2, 3, 0), "t") == (6, 0, 0)
+    for ok in (t[:, :8], t[1:2, 3:8], torch.zeros(2, 3, 4), torch.zeros(5), torch.zeros(0, 7)):
+        with pytest.raises(ValueError, match="CUDA"):  # past the checks of the shape
+            l8.quantize(ok)
     for bad in (t.t(), t[:, ::2], t[:1].expand(6, 20), torch.zeros(2, 3, 4).transpose(0, 1), torch.zeros(())):
-        with pytest.raises(ValueError):
-            l8._rows(bad, "t")
+        with pytest.raises(ValueError, match="stride|overlap|contiguous|dimension"):
+            l8.quantize(bad)
+    for bad in (None, 3, [1.0]):
+        with pytest.raises(ValueError, match="tensor"):
+            l8.quantize(bad)
+    with pytest.raises(ValueError, match="fp32 or bf16"):
+        l8.quantize(t.half())
+    with pytest.raises(ValueError, match="dtype"):
+        l8.dequantize(l8.Q8(torch.zeros(4, 8, dtype=torch.int8), torch.ones(4)), "bf16")
+    with pytest.raises(ValueError, match="fp32 or bf16"):
+        l8.dequantize(l8.Q8(torch.zeros(4, 8, dtype=torch.int8), torch.ones(4)), torch.float16)
+
+
+def test_abi_errors_become_exceptions():
+    from matrix_aware_optimizer_muon_amd import _linear8
+    with pytest.raises(ValueError, match="number of arguments"):
+        _linear8.quantize()
+    with pytest.raises(TypeError):
+        l8.rmsnorm(torch.zeros(4, 8), torch.ones(8), eps="x")
