@@ -45,7 +45,7 @@ def test_norm_refusals(kw, want):
     assert norm(**kw) == want
 
 
-def back(dy=P, lddy=64, h=P, ldh=64, hs=0, rstd=P, w=P, dh=0, lddh=0, dtype=1, rows=4, cols=64, dx=P,
+def back(dy=P, lddy=64, h=P, ldh=64, hs=0, rstd=P, w=P, dh=0, lddh=0, dtype=1, rows=4000, cols=64, dx=P,
          lddx=64, dw=P, ws=P, wsb=1 << 20):
     return abi().muon_rmsnorm_backward(dy, lddy, h, ldh, hs, rstd, w, dh, lddh, dtype, rows, cols, dx,
                                            lddx, dw, ws, wsb, None)
