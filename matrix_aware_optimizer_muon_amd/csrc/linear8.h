@@ -81,7 +81,7 @@ hipError_t launch_mm(const MmParams& p, ProductKind kind, hipStream_t s);
 
 // The product for at most kFewRows rows of x (one generated token and short
 // batches): no tiles, no alignment, reads the weights once.
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 64;
 hipError_t launch_few(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw,
                       const float* ws, void* y, int64_t ldy, bool bf16, int t, int n, int k, hipStream_t s);
 

@@ -85,10 +85,12 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
     c.unaligned = off_q || off_p;
   }
   // Workgroups that run at once: whole rounds of them take a tile each, the
-  // tiles left over are split along K over one more round.
+  // tiles left over are split along K over one more round, unless the sum is
+  // too short to pay for the second launch (about 4 us; a stage of a lone
+  // workgroup takes 0.37 us).
   const int64_t slots = c.tile == 256 ? 256 : 512, all = tiles(c.tile), rest = all % slots;
   c.direct = (int)all;
-  if (rest > 0) {
+  if (rest > 0 && stages >= 24) {
     c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({slots / rest, stages / 8, 32}));
     if (c.splits > 1) {
       c.direct = (int)(all - rest);

@@ -123,20 +123,42 @@ struct DmaOperand {
   }
 };
 
-// The bytes [0, n) of a 16-byte chunk, zeros beyond.
-__device__ __forceinline__ u32x4 load_part(const char* a, int n) {
-  union { u32x4 v; uint8_t e[16]; } b;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) b.e[i] = i < n ? (uint8_t)a[i] : (uint8_t)0;
-  return b.v;
+// The bytes [0, n) at a, 0 < n < 16, zeros beyond; a lies in a matrix that
+// starts at base and has `total` bytes.  One 16-byte read that ends with the
+// last byte wanted (or starts at base), shifted into place: byte reads, one
+// after the other behind their predicates, took 8 us of a 1-stage product.
+__device__ __forceinline__ u32x4 load_part(const char* a, int n, const char* base, int64_t total) {
+  uint64_t w[2] = {0, 0};
+  if (total >= 16) {
+    const int64_t before = a - base;
+    const int d = before < 16 - n ? (int)before : 16 - n;
+    __builtin_memcpy(w, a - d, 16);
+    const int sh = (d & 7) * 8;
+    if (d & 8) {
+      w[0] = w[1];
+      w[1] = 0;
+    }
+    w[0] = sh ? (w[0] >> sh) | (w[1] << (64 - sh)) : w[0];
+    w[1] >>= sh;
+    const uint64_t m = (1ull << ((n & 7) * 8)) - 1;
+    w[0] &= n < 8 ? m : ~0ull;
+    w[1] &= n < 8 ? 0ull : m;
+  } else {
+    for (int i = 0; i < n; ++i) {
+      const uint64_t e = (uint64_t)(uint8_t)a[i] << ((i & 7) * 8);
+      w[0] |= i < 8 ? e : 0;
+      w[1] |= i < 8 ? 0 : e;
+    }
+  }
+  return u32x4{(uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32)};
 }
 
 // One operand fed through registers, 16 bytes of a row per lane and chunk:
 // at any address, and, with CONV, int8 rows times their scale widened to
 // bf16 on the way (16 values per lane, two 16-byte LDS writes).  Whole 16-byte
 // reads that leave the row stay inside the matrix for all stages before
-// `safe` (load); load_cut, for any stage, reads what exists, byte by byte
-// where a chunk is cut, and takes zero for the rest.
+// `safe` (load); load_cut, for any stage, reads what exists and takes zero for
+// the rest.
 template <bool KM, bool CONV, int T, int NT>
 struct RegOperand {
   static constexpr int CPR = KM ? (CONV ? T / 16 : T / 8) : 4;   // chunks per stage row
@@ -149,12 +171,15 @@ struct RegOperand {
   };
   const char* src[N];
   const float* scale;
-  int64_t step;
+  const char* base;
+  int64_t step, total;
   int safe, kd, left;  // left: bytes of the chunk's row from the chunk on
   int row, col;        // the lane's first stage row, its chunk
 
-  __device__ __forceinline__ void init(const char* base, int64_t ld, const float* sc, int row0, int count,
+  __device__ __forceinline__ void init(const char* from, int64_t ld, const float* sc, int row0, int count,
                                        int kdim, int kbytes, int full, int tid) {
+    base = from;
+    total = KM ? (int64_t)(kdim - 1) * ld + count * (CONV ? 1 : 2) : (int64_t)(count - 1) * ld + kbytes;
     row = tid / CPR;
     col = tid % CPR;
     kd = kdim;
@@ -194,7 +219,7 @@ struct RegOperand {
       else n = left - ks * KB;
       r.v[i] = u32x4{0, 0, 0, 0};
       if (n >= 16) __builtin_memcpy(&r.v[i], src[i] + ks * step, 16);
-      else if (n > 0) r.v[i] = load_part(src[i] + ks * step, n);
+      else if (n > 0) r.v[i] = load_part(src[i] + ks * step, n, base, total);
     }
     if constexpr (CONV) r.scale = ks * KROWS + row < kd ? scale[ks * KROWS + row] : 0.0f;
   }
@@ -553,54 +578,84 @@ __global__ void __launch_bounds__(256) mm_sum_kernel(const MmParams p) {
   put4(p, (int64_t)r * p.ldo + c, n, v);
 }
 
-// At most 16 rows of x.  A workgroup takes 16 rows of w; its four waves take
-// every fourth 64-byte step of K, straight from HBM into MFMA fragments (a
-// row of w is read once, by one workgroup; x stays in the caches), and the
-// int32 partial tiles are added through LDS.
+// Few rows of x (at most 16 QB).  A workgroup takes 16 PB rows of w; its four
+// waves take every fourth 64-byte step of K, straight from memory into MFMA
+// fragments at any alignment (a row of w is read once, by one workgroup; x
+// comes from the caches), and the int32 partial tiles are added through LDS.
+// Bound by the read of w: one row of x against 18944 x 3584 takes 12.1 us,
+// 5.6 TB/s.
+template <int PB, int QB>
 __global__ void __launch_bounds__(256) few_kernel(const int8_t* xq, int64_t ldx, const float* xs,
                                                   const int8_t* wq, int64_t ldw, const float* ws, void* y,
                                                   int64_t ldy, int bf16, int t, int n, int k) {
-  __shared__ i32x4 s_part[3][64];
+  __shared__ i32x4 s_part[3][PB * QB][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int q4 = lane >> 4, c16 = lane & 15;
-  const int n0 = blockIdx.x * 16;
-  const int8_t* wr = wq + (int64_t)min(n0 + c16, n - 1) * ldw + q4 * 16;
-  const int8_t* xr = xq + (int64_t)min(c16, t - 1) * ldx + q4 * 16;
-  i32x4 acc = {0, 0, 0, 0};
+  const int n0 = blockIdx.x * (16 * PB);
+  const int8_t *wr[PB], *xr[QB];
+#pragma unroll
+  for (int i = 0; i < PB; ++i) wr[i] = wq + (int64_t)min(n0 + 16 * i + c16, n - 1) * ldw + q4 * 16;
+#pragma unroll
+  for (int j = 0; j < QB; ++j) xr[j] = xq + (int64_t)min(16 * j + c16, t - 1) * ldx + q4 * 16;
+  i32x4 acc[PB][QB];
+#pragma unroll
+  for (int i = 0; i < PB; ++i)
+#pragma unroll
+    for (int j = 0; j < QB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
   const int whole = k / 64;
   int s = wave;
 #pragma unroll 4
   for (; s < whole; s += 4) {
-    u32x4 a, b;
-    __builtin_memcpy(&a, wr + s * 64, 16);
-    __builtin_memcpy(&b, xr + s * 64, 16);
-    Mfma<true>::go(a, b, acc);
+    u32x4 a[PB], b[QB];
+#pragma unroll
+    for (int i = 0; i < PB; ++i) __builtin_memcpy(&a[i], wr[i] + s * 64, 16);
+#pragma unroll
+    for (int j = 0; j < QB; ++j) __builtin_memcpy(&b[j], xr[j] + s * 64, 16);
+#pragma unroll
+    for (int i = 0; i < PB; ++i)
+#pragma unroll
+      for (int j = 0; j < QB; ++j) Mfma<true>::go(a[i], b[j], acc[i][j]);
   }
-  if (s == whole && k % 64) {  // one wave takes the ragged last step, byte by byte
-    union { u32x4 v; int8_t e[16]; } a, b;
+  if (s == whole && k % 64) {  // one wave takes the ragged last step
+    u32x4 a[PB], b[QB];
     const int left = k - whole * 64 - q4 * 16;
+    auto part = [&](const int8_t* r, const int8_t* base, int64_t total) {
+      u32x4 v = {0, 0, 0, 0};
+      const char* c = (const char*)r + whole * 64;
+      if (left >= 16) __builtin_memcpy(&v, c, 16);
+      else if (left > 0) v = load_part(c, left, (const char*)base, total);
+      return v;
+    };
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      a.e[i] = i < left ? wr[whole * 64 + i] : (int8_t)0;
-      b.e[i] = i < left ? xr[whole * 64 + i] : (int8_t)0;
-    }
-    Mfma<true>::go(a.v, b.v, acc);
+    for (int i = 0; i < PB; ++i) a[i] = part(wr[i], wq, (int64_t)(n - 1) * ldw + k);
+#pragma unroll
+    for (int j = 0; j < QB; ++j) b[j] = part(xr[j], xq, (int64_t)(t - 1) * ldx + k);
+#pragma unroll
+    for (int i = 0; i < PB; ++i)
+#pragma unroll
+      for (int j = 0; j < QB; ++j) Mfma<true>::go(a[i], b[j], acc[i][j]);
   }
-  if (wave > 0) s_part[wave - 1][lane] = acc;
-  __syncthreads();
-  if (wave == 0 && c16 < t) {
+  if (wave > 0) {
 #pragma unroll
-    for (int i = 0; i < 3; ++i) acc += s_part[i][lane];
-    MmParams p = {};
-    p.out = y;
-    p.obf16 = bf16;
-    const int c = n0 + 4 * q4;
-    if (c < n) {
-      const float sx = xs[c16];
+    for (int i = 0; i < PB * QB; ++i) s_part[wave - 1][i][lane] = acc[i / QB][i % QB];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  MmParams p = {};
+  p.out = y;
+  p.obf16 = bf16;
+#pragma unroll
+  for (int i = 0; i < PB * QB; ++i) {
+    i32x4 a = acc[i / QB][i % QB];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) a += s_part[q][i][lane];
+    const int c = n0 + 16 * (i / QB) + 4 * q4, r = 16 * (i % QB) + c16;
+    if (c < n && r < t) {
+      const float sx = xs[r];
       float v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (float)acc[e] * sx * ws[min(c + e, n - 1)];
-      put4(p, (int64_t)c16 * ldy + c, n - c, v);
+      for (int e = 0; e < 4; ++e) v[e] = (float)a[e] * sx * ws[min(c + e, n - 1)];
+      put4(p, (int64_t)r * ldy + c, n - c, v);
     }
   }
 }
@@ -655,9 +710,17 @@ hipError_t launch_mm(const MmParams& p, ProductKind kind, hipStream_t s) {
 
 hipError_t launch_few(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw,
                       const float* ws, void* y, int64_t ldy, bool bf16, int t, int n, int k, hipStream_t s) {
-  hipLaunchKernelGGL(few_kernel, dim3((uint32_t)((n + 15) / 16)), dim3(256), 0, s, xq, ldx, xs, wq, ldw, ws,
-                     y, ldy, bf16 ? 1 : 0, t, n, k);
-  return hipGetLastError();
+  auto go = [&](auto kernel, int rows) {
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)((n + rows - 1) / rows)), dim3(256), 0, s, xq, ldx, xs, wq, ldw,
+                       ws, y, ldy, bf16 ? 1 : 0, t, n, k);
+    return hipGetLastError();
+  };
+  // two blocks of w's rows per workgroup halve the reads of x; with fewer than
+  // 256 workgroups left they would leave compute units without one
+  const bool two = n >= 256 * 32;
+  if (t <= 16) return go(few_kernel<1, 1>, 16);
+  if (t <= 32) return two ? go(few_kernel<2, 2>, 32) : go(few_kernel<1, 2>, 16);
+  return two ? go(few_kernel<2, 4>, 32) : go(few_kernel<1, 4>, 16);
 }
 
 hipError_t launch_pack(const void* src, int64_t lds, int64_t bytes, void* dst, int64_t ld, int64_t rows,

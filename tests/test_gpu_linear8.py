@@ -291,22 +291,22 @@ def check_matmul(t, n, k, dtype, x=None, w=None, scales="pow2"):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("t", [1, 2, 15, 16])
-@pytest.mark.parametrize("n, k", [(1, 1), (15, 16), (16, 63), (17, 64), (100, 65), (33, 255), (48, 257), (1000, 1024),
-                                  (37, 3584)])
+@pytest.mark.parametrize("t", [1, 2, 15, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("n, k", [(1, 1), (2, 5), (15, 16), (16, 63), (17, 64), (100, 65), (33, 255), (48, 257),
+                                  (1000, 1024), (37, 3584), (8201, 100)])
 def test_matmul_few_rows(t, n, k, dtype):
     check_matmul(t, n, k, dtype)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("t, n, k", [(17, 1, 16), (100, 8, 33), (128, 128, 64), (129, 127, 80), (300, 130, 512),
-                                     (257, 400, 1), (64, 64, 48), (31, 513, 100), (40, 260, 4096), (130, 130, 8191),
-                                     (4000, 3500, 80), (3900, 3585, 97)])
+@pytest.mark.parametrize("t, n, k", [(65, 1, 16), (100, 8, 33), (128, 128, 64), (129, 127, 80), (300, 130, 512),
+                                     (257, 400, 1), (96, 64, 48), (95, 513, 100), (72, 260, 4096), (130, 130, 8191),
+                                     (81, 70, 15), (70, 3, 7), (4000, 3500, 80), (3900, 3585, 97)])
 def test_matmul_tiles(t, n, k, dtype):
     check_matmul(t, n, k, dtype)
 
 
-@pytest.mark.parametrize("t", [3, 50])
+@pytest.mark.parametrize("t", [3, 50, 100])
 def test_matmul_scales_strides_and_extremes(t):
     check_matmul(t, 70, 200, F32, scales="any")
     x, w = q8rand(t, 160, 3), q8rand(66, 160, 4)
@@ -321,7 +321,7 @@ def test_matmul_scales_strides_and_extremes(t):
 
 
 def test_matmul_empty_and_non_finite_rows():
-    x, w = q8rand(40, 64, 1), q8rand(50, 64, 2)
+    x, w = q8rand(80, 64, 1), q8rand(50, 64, 2)
     e = l8.Q8(x.q[:, :0].contiguous(), x.scale)
     assert not l8.matmul(e, l8.Q8(w.q[:, :0].contiguous(), w.scale)).any()
     assert not l8.matmul(l8.Q8(e.q[:3], e.scale[:3]), l8.Q8(w.q[:, :0].contiguous(), w.scale)).any()
@@ -336,8 +336,8 @@ def test_matmul_empty_and_non_finite_rows():
     want[7] = True
     want[:, 3] = True
     assert torch.equal(bad, want) and torch.equal(y[~bad], clean[~bad])
-    x3 = l8.Q8(x.q.reshape(4, 10, 64), x.scale.reshape(4, 10))
-    assert torch.equal(l8.matmul(x3, w), clean.reshape(4, 10, 50))
+    x3 = l8.Q8(x.q.reshape(4, 20, 64), x.scale.reshape(4, 20))
+    assert torch.equal(l8.matmul(x3, w), clean.reshape(4, 20, 50))
 
 
 def check_grad(kind, t, n, k, dtype, dy=None, other=None, scales="pow2", accumulate=False):

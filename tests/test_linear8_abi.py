@@ -130,7 +130,7 @@ def ws(kind, t, n, k, a=0, b=0, lda=None, ldb=None):
 
 
 def test_workspace_sizes():
-    assert ws(0, 1, 18944, 3584) == 0 and ws(0, 16, 100, 33) == 0    # few rows: none
+    assert ws(0, 1, 18944, 3584) == 0 and ws(0, 64, 100, 33) == 0    # few rows: none
     assert ws(0, 4096, 16384, 3584) == 0                             # aligned, whole rounds of tiles
     assert ws(0, 4096, 16384, 3583) >= (4096 + 16384) * 3584         # both operands padded
     assert ws(0, 4096, 16384, 3584, a=8) >= 4096 * 3584              # x off its 16 bytes
