@@ -64,6 +64,7 @@ struct MmParams {
   const char* P;
   const char* Q;
   int64_t ldp, ldq;         // bytes
+  int padp, padq;           // bytes that may be read after the last row
   int np, nq, kd;           // output columns, output rows, contraction
   int tile;                 // 256 or 128
   bool unaligned;           // an operand that the DMA would read has rows off 16 bytes (tile 128)
@@ -79,9 +80,11 @@ struct MmParams {
 
 hipError_t launch_mm(const MmParams& p, ProductKind kind, hipStream_t s);
 
-// The product for at most kFewRows rows of x (one generated token and short
-// batches): no tiles, no alignment, reads the weights once.
-constexpr int kFewRows = 64;
+// The product for few rows of x (generated tokens, short batches; at most
+// 64): no tiles, no alignment, reads the weights once.  From 33 rows on the
+// reads of x count as well: measured against the tile kernel at 64 rows, 10
+// against 15 us for 4000 x 4000 weights, 32 against 27 us for 18944 x 3584.
+inline bool few_rows(int64_t t, int64_t n, int64_t k) { return t <= 32 || (t <= 64 && n * k <= 1 << 25); }
 hipError_t launch_few(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw,
                       const float* ws, void* y, int64_t ldy, bool bf16, int t, int n, int k, hipStream_t s);
 

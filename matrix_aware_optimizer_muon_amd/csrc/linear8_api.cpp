@@ -33,12 +33,13 @@ muon_status row_sizes(int64_t rows, int64_t cols) {
   return MUON_OK;
 }
 
-// How a product runs.  `few`: the kernel for at most kFewRows rows of x.
+// How a product runs.  `few`: the kernel for few rows of x.
 struct Choice {
   bool few = false;
   bool unaligned = false;          // read through registers (tile 128)
   bool pack_q = false, pack_p = false;
   int64_t ldq = 0, ldp = 0;        // bytes, as the tile kernel reads them
+  int padq = 0, padp = 0;          // readable after the last row
   int64_t at_q = 0, at_p = 0, at_part = 0;
   int tile = 128, splits = 1, direct = 0;
   int np = 0, nq = 0, kd = 0;
@@ -49,7 +50,7 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
               int64_t n, int64_t k) {
   Choice c;
   const bool i8 = kind == MUON_Q8_MATMUL;
-  if (i8 && t <= kFewRows) {
+  if (i8 && few_rows(t, n, k)) {
     c.few = true;
     return c;
   }
@@ -71,24 +72,31 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
   if (c.tile == 256) {
     c.pack_q = off_q;
     c.pack_p = off_p;
-    if (c.pack_q) {
-      c.ldq = up(a_cols * sa, 16);
-      c.at_q = c.bytes;
-      c.bytes += up(a_rows * c.ldq, 256);
-    }
-    if (c.pack_p) {
-      c.ldp = up(b_cols, 16);
-      c.at_p = c.bytes;
-      c.bytes += up(b_rows * c.ldp, 256);
-    }
   } else {
+    // through registers, from matrices of at least 16 bytes
     c.unaligned = off_q || off_p;
+    c.pack_q = c.unaligned && (a_rows - 1) * c.ldq + a_cols * sa < 16;
+    c.pack_p = (c.unaligned || !i8) && (b_rows - 1) * c.ldp + b_cols < 16;
+  }
+  if (c.kd == 0) c.pack_q = c.pack_p = false;
+  if (c.pack_q) {
+    c.ldq = up(a_cols * sa, 16);
+    c.padq = (int)(c.ldq - a_cols * sa);
+    c.at_q = c.bytes;
+    c.bytes += up(a_rows * c.ldq, 256);
+  }
+  if (c.pack_p) {
+    c.ldp = up(b_cols, 16);
+    c.padp = (int)(c.ldp - b_cols);
+    c.at_p = c.bytes;
+    c.bytes += up(b_rows * c.ldp, 256);
   }
   // Workgroups that run at once: whole rounds of them take a tile each, the
   // tiles left over are split along K over one more round, unless the sum is
-  // too short to pay for the second launch (about 4 us; a stage of a lone
-  // workgroup takes 0.37 us).
-  const int64_t slots = c.tile == 256 ? 256 : 512, all = tiles(c.tile), rest = all % slots;
+  // too short to pay for the second launch (about 4 us).  128-wide tiles run
+  // two to a compute unit.
+  const int64_t all = tiles(c.tile);
+  const int64_t slots = c.tile == 256 ? 256 : 512, rest = all % slots;
   c.direct = (int)all;
   if (rest > 0 && stages >= 24) {
     c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({slots / rest, stages / 8, 32}));
@@ -139,6 +147,8 @@ muon_status run_product(muon_q8_product kind, const void* a, int64_t lda, const 
   p.P = c.pack_p ? w + c.at_p : (const char*)b;
   p.ldq = c.ldq;
   p.ldp = c.ldp;
+  p.padq = c.padq;
+  p.padp = c.padp;
   p.np = c.np;
   p.nq = c.nq;
   p.kd = c.kd;
@@ -154,11 +164,11 @@ muon_status run_product(muon_q8_product kind, const void* a, int64_t lda, const 
   p.accumulate = accumulate;
   p.part = c.splits > 1 ? (float*)(w + c.at_part) : nullptr;
   hipError_t e = hipSuccess;
-  if (c.pack_q && c.kd > 0) {
+  if (c.pack_q) {
     const int64_t sa = i8 ? 1 : 2;
     e = launch_pack(a, t > 1 ? lda * sa : 0, a_cols * sa, w + c.at_q, c.ldq, t, s);
   }
-  if (e == hipSuccess && c.pack_p && c.kd > 0) e = launch_pack(b, ldb, k, w + c.at_p, c.ldp, b_rows, s);
+  if (e == hipSuccess && c.pack_p) e = launch_pack(b, ldb, k, w + c.at_p, c.ldp, b_rows, s);
   if (e == hipSuccess)
     e = launch_mm(p, i8 ? KIND_I8 : kind == MUON_Q8_GRAD_INPUT ? KIND_DX : KIND_DW, s);
   return hip(e);

@@ -14,8 +14,8 @@
 //
 // Tiles: 256 x 256 (8 waves, 2 x 4, each 128 x 64) or 128 x 128 (4 waves,
 // 2 x 2, each 64 x 64).  A stage is 64 bytes of K per operand row (64 int8,
-// 32 bf16): one MFMA K step.  Stages stream through a four-deep LDS ring
-// filled by direct global->LDS loads; one barrier per stage, placed so that it
+// 32 bf16): one MFMA K step.  Stages stream through a four-deep LDS
+// ring filled by direct global->LDS loads or from registers; one barrier per stage, placed so that it
 // publishes the next stage and retires the reads of the current one, and a
 // constant vmcnt (stages past the end are loaded like any other, from valid
 // addresses, and never read).
@@ -33,7 +33,6 @@ namespace {
 
 constexpr int KB = 64;        // bytes of K per stage and contiguous row
 constexpr int KROWS = 32;     // rows of K per stage of a K-major operand
-constexpr int STAGES = 4;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_ptr_t;
@@ -123,33 +122,26 @@ struct DmaOperand {
   }
 };
 
-// The bytes [0, n) at a, 0 < n < 16, zeros beyond; a lies in a matrix that
-// starts at base and has `total` bytes.  One 16-byte read that ends with the
-// last byte wanted (or starts at base), shifted into place: byte reads, one
-// after the other behind their predicates, took 8 us of a 1-stage product.
-__device__ __forceinline__ u32x4 load_part(const char* a, int n, const char* base, int64_t total) {
-  uint64_t w[2] = {0, 0};
-  if (total >= 16) {
-    const int64_t before = a - base;
-    const int d = before < 16 - n ? (int)before : 16 - n;
-    __builtin_memcpy(w, a - d, 16);
-    const int sh = (d & 7) * 8;
-    if (d & 8) {
-      w[0] = w[1];
-      w[1] = 0;
-    }
-    w[0] = sh ? (w[0] >> sh) | (w[1] << (64 - sh)) : w[0];
-    w[1] >>= sh;
-    const uint64_t m = (1ull << ((n & 7) * 8)) - 1;
-    w[0] &= n < 8 ? m : ~0ull;
-    w[1] &= n < 8 ? 0ull : m;
-  } else {
-    for (int i = 0; i < n; ++i) {
-      const uint64_t e = (uint64_t)(uint8_t)a[i] << ((i & 7) * 8);
-      w[0] |= i < 8 ? e : 0;
-      w[1] |= i < 8 ? 0 : e;
-    }
+// The bytes [0, n) at a (none: n <= 0, all: n >= 16), zeros beyond.  last: the
+// last place of the matrix where 16 bytes can be read; the bytes wanted lie
+// before its end.  One read at any address, shifted and masked into place,
+// without a branch: byte reads behind their predicates took 8 us of a
+// one-stage product.
+__device__ __forceinline__ u32x4 load_part(const char* a, int n, const char* last) {
+  const char* at = a < last ? a : last;
+  const int d = (int)(a - at) & 15;  // (over 15 only where n <= 0)
+  uint64_t w[2];
+  __builtin_memcpy(w, at, 16);
+  const int sh = (d & 7) * 8;
+  if (d & 8) {
+    w[0] = w[1];
+    w[1] = 0;
   }
+  w[0] = sh ? (w[0] >> sh) | (w[1] << (64 - sh)) : w[0];
+  w[1] >>= sh;
+  const uint64_t m = (1ull << ((n & 7) * 8)) - 1;  // the cut half's bytes
+  w[0] &= n >= 8 ? ~0ull : n > 0 ? m : 0ull;
+  w[1] &= n >= 16 ? ~0ull : n > 8 ? m : 0ull;
   return u32x4{(uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32)};
 }
 
@@ -158,7 +150,8 @@ __device__ __forceinline__ u32x4 load_part(const char* a, int n, const char* bas
 // bf16 on the way (16 values per lane, two 16-byte LDS writes).  Whole 16-byte
 // reads that leave the row stay inside the matrix for all stages before
 // `safe` (load); load_cut, for any stage, reads what exists and takes zero for
-// the rest.
+// the rest.  The matrix has at least 16 bytes (`pad` of them may follow its
+// last row).
 template <bool KM, bool CONV, int T, int NT>
 struct RegOperand {
   static constexpr int CPR = KM ? (CONV ? T / 16 : T / 8) : 4;   // chunks per stage row
@@ -171,15 +164,15 @@ struct RegOperand {
   };
   const char* src[N];
   const float* scale;
-  const char* base;
-  int64_t step, total;
+  const char* last;
+  int64_t step;
   int safe, kd, left;  // left: bytes of the chunk's row from the chunk on
   int row, col;        // the lane's first stage row, its chunk
 
-  __device__ __forceinline__ void init(const char* from, int64_t ld, const float* sc, int row0, int count,
-                                       int kdim, int kbytes, int full, int tid) {
-    base = from;
-    total = KM ? (int64_t)(kdim - 1) * ld + count * (CONV ? 1 : 2) : (int64_t)(count - 1) * ld + kbytes;
+  __device__ __forceinline__ void init(const char* base, int64_t ld, int pad, const float* sc, int row0,
+                                       int count, int kdim, int kbytes, int full, int tid) {
+    last = base - 16 + pad +
+           (KM ? (int64_t)(kdim - 1) * ld + count * (CONV ? 1 : 2) : (int64_t)(count - 1) * ld + kbytes);
     row = tid / CPR;
     col = tid % CPR;
     kd = kdim;
@@ -217,11 +210,13 @@ struct RegOperand {
       int n;
       if constexpr (KM) n = ks * KROWS + row + i * (KROWS / N) < kd ? left : 0;
       else n = left - ks * KB;
-      r.v[i] = u32x4{0, 0, 0, 0};
-      if (n >= 16) __builtin_memcpy(&r.v[i], src[i] + ks * step, 16);
-      else if (n > 0) r.v[i] = load_part(src[i] + ks * step, n, base, total);
+      r.v[i] = load_part(src[i] + ks * step, n, last);
     }
-    if constexpr (CONV) r.scale = ks * KROWS + row < kd ? scale[ks * KROWS + row] : 0.0f;
+    if constexpr (CONV) {
+      const int k = ks * KROWS + row;
+      const float f = scale[min(k, kd - 1)];
+      r.scale = k < kd ? f : 0.0f;
+    }
   }
   // Piece q of PIECES of a stage's way into LDS, so that the caller can put
   // MFMAs between them.
@@ -231,7 +226,10 @@ struct RegOperand {
   };
   __device__ __forceinline__ void store(const Regs& r, Wide& w, char* stage, int q) const {
     if constexpr (CONV) {
-      const uint32_t b = r.v[0][q];
+      // (opaque: the compiler otherwise takes the bytes apart at the load,
+      // carries 16 registers for 4 and waits for the load to do so)
+      uint32_t b = r.v[0][q];
+      asm("" : "+v"(b));
       float f[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(b >> (8 * e)) * r.scale;
@@ -340,9 +338,12 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
   typedef RegOperand<QKM, false, T, 64 * NW> RegQ;
   constexpr int DP = PREG ? 0 : DmaP::NDMA, DPS = DP + (QREG ? 0 : DmaQ::NDMA);
   constexpr int OPB = T * KB;                    // one operand's stage in LDS
+  constexpr int D = 4;                           // stages of a ring
   constexpr int RS = 2;                          // register sets in flight
-  __shared__ __attribute__((aligned(1024))) char sp_[STAGES * OPB];
-  __shared__ __attribute__((aligned(1024))) char sq_[STAGES * OPB];
+  // (two objects: the compiler then knows that a write to one is no write to
+  // the other)
+  __shared__ __attribute__((aligned(1024))) char sp_[D * OPB];
+  __shared__ __attribute__((aligned(1024))) char sq_[D * OPB];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -367,159 +368,168 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
   constexpr int KE = I8K ? 64 : 32;              // K elements per stage
   const int full = p.kd / KE;
   const int nk = (p.kd + KE - 1) / KE;
-  const int k0 = (int)((int64_t)nk * split / splits), k1 = (int)((int64_t)nk * (split + 1) / splits);
+  int k0 = 0, k1 = nk;
+  if (splits > 1) {
+    k0 = (int)((int64_t)nk * split / splits);
+    k1 = (int)((int64_t)nk * (split + 1) / splits);
+  }
+  const int steps = k1 - k0;
   const int kbytes = p.kd * (I8K ? 1 : 2);
-
-  DmaP dp;
-  DmaQ dq;
-  RegP gp;
-  RegQ gq;
-  if constexpr (PREG) gp.init(p.P, p.ldp, p.sp, tp * T, p.np, p.kd, kbytes, full, tid);
-  else dp.init(p.P, p.ldp, tp * T, p.np, p.kd, kbytes, full, tid);
-  if constexpr (QREG) gq.init(p.Q, p.ldq, nullptr, tq * T, p.nq, p.kd, kbytes, full, tid);
-  else dq.init(p.Q, p.ldq, tq * T, p.nq, p.kd, kbytes, full, tid);
-  auto dma = [&](int q, int buf, int ks) {
-    if (q < DP) dp.load(q, sp_ + buf * OPB, ks, full, wave);
-    else dq.load(q - DP, sq_ + buf * OPB, ks, full, wave);
-  };
-  typename RegP::Regs rp[RS];
-  typename RegQ::Regs rq[RS];
-  typename RegP::Wide wp8;
-  typename RegQ::Wide wq8;
-  auto fetch = [&](auto cut, int set, int ks) {
-    if constexpr (PREG) {
-      if constexpr (decltype(cut)::value) gp.load_cut(rp[set], ks);
-      else gp.load(rp[set], ks);
-    }
-    if constexpr (QREG) {
-      if constexpr (decltype(cut)::value) gq.load_cut(rq[set], ks);
-      else gq.load(rq[set], ks);
-    }
-  };
-  // pieces of a register set's way into LDS
-  constexpr int PP = PREG ? RegP::PIECES : 0, PQ = QREG ? RegQ::PIECES : 0;
-  auto put = [&](int set, int buf, int q) {
-    if (q < PP) gp.store(rp[set], wp8, sp_ + buf * OPB, q);
-    else if (q < PP + PQ) gq.store(rq[set], wq8, sq_ + buf * OPB, q - PP);
-  };
-  Reader<PKM, T> fp;
-  Reader<QKM, T> fq;
-  fp.init(wp * (T / 2), q4, c16);
-  fq.init(wq * (T / WQ), q4, c16);
 
   Acc acc[FP][FQ];
 #pragma unroll
   for (int i = 0; i < FP; ++i)
 #pragma unroll
     for (int j = 0; j < FQ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
-  u32x4 fa[FP], fb0[FQ], fb1[FQ];
 
-  // DMA: a stage's DPS instructions go out in two halves, so that every run
-  // of MFMAs carries the same share: the first half of stage kt + 4 in the
-  // second half of step kt (its buffer is released by that step's barrier),
-  // the rest in the first half of step kt + 1.
-  // Registers: stage kt + 2 goes into LDS in the second half of step kt, and
-  // its set is loaded again with stage kt + 4, two steps ahead of its use.
-#pragma unroll
-  for (int st = 0; st < STAGES; ++st)
-#pragma unroll
-    for (int q = 0; q < DPS; ++q)
-      if (st < STAGES - 1 || q < DPS / 2) dma(q, st, k0 + st);
-  constexpr int PIECES_ALL = PP + PQ;
-  if constexpr (PIECES_ALL > 0) {
-    // stages 0 .. 3 in flight together; everything has landed before the
-    // loop, so that the waits inside it only count the loop's own loads
-    typename RegP::Regs rp0[2];
-    typename RegQ::Regs rq0[2];
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      if constexpr (PREG) gp.load_cut(rp0[st], k0 + st);
-      if constexpr (QREG) gq.load_cut(rq0[st], k0 + st);
-    }
-#pragma unroll
-    for (int st = 0; st < RS; ++st) fetch(Cut<true>(), st, k0 + 2 + st);
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
-#pragma unroll
-      for (int q = 0; q < PP; ++q) gp.store(rp0[st], wp8, sp_ + st * OPB, q);
-#pragma unroll
-      for (int q = 0; q < PQ; ++q) gq.store(rq0[st], wq8, sq_ + st * OPB, q);
-    }
-    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
-  } else {
-    __builtin_amdgcn_s_waitcnt(wait_imm(2 * DPS + DPS / 2, 15));
-  }
-  barrier();
-#pragma unroll
-  for (int f = 0; f < H; ++f) fa[f] = fp.get(sp_, f);
-#pragma unroll
-  for (int f = 0; f < FQ; ++f) fb0[f] = fq.get(sq_, f);
+  if (steps > 0) {  // (an empty sum reads nothing)
+    DmaP dp;
+    DmaQ dq;
+    RegP gp;
+    RegQ gq;
+    if constexpr (PREG) gp.init(p.P, p.ldp, p.padp, p.sp, tp * T, p.np, p.kd, kbytes, full, tid);
+    else dp.init(p.P, p.ldp, tp * T, p.np, p.kd, kbytes, full, tid);
+    if constexpr (QREG) gq.init(p.Q, p.ldq, p.padq, nullptr, tq * T, p.nq, p.kd, kbytes, full, tid);
+    else dq.init(p.Q, p.ldq, tq * T, p.nq, p.kd, kbytes, full, tid);
+    auto dma = [&](int q, int st) {  // instruction q of stage k0 + st
+      if (q < DP) dp.load(q, sp_ + (st & (D - 1)) * OPB, k0 + st, full, wave);
+      else dq.load(q - DP, sq_ + (st & (D - 1)) * OPB, k0 + st, full, wave);
+    };
+    typename RegP::Regs rp[RS];
+    typename RegQ::Regs rq[RS];
+    typename RegP::Wide wp8;
+    typename RegQ::Wide wq8;
+    auto fetch = [&](auto cut, typename RegP::Regs& a, typename RegQ::Regs& b, int st) {
+      if constexpr (PREG) {
+        if constexpr (decltype(cut)::value) gp.load_cut(a, k0 + st);
+        else gp.load(a, k0 + st);
+      }
+      if constexpr (QREG) {
+        if constexpr (decltype(cut)::value) gq.load_cut(b, k0 + st);
+        else gq.load(b, k0 + st);
+      }
+    };
+    // pieces of a register set's way into LDS
+    constexpr int PP = PREG ? RegP::PIECES : 0, PQ = QREG ? RegQ::PIECES : 0, PIECES = PP + PQ;
+    auto put = [&](const typename RegP::Regs& a, const typename RegQ::Regs& b, int st, int q) {
+      if (q < PP) gp.store(a, wp8, sp_ + (st & (D - 1)) * OPB, q);
+      else if (q < PIECES) gq.store(b, wq8, sq_ + (st & (D - 1)) * OPB, q - PP);
+    };
+    Reader<PKM, T> fp;
+    Reader<QKM, T> fq;
+    fp.init(wp * (T / 2), q4, c16);
+    fq.init(wq * (T / WQ), q4, c16);
+    u32x4 fa[FP], fb0[FQ], fb1[FQ];
 
-  auto step = [&](auto cut, int kt, int set, u32x4* fb, u32x4* fbn) {  // kt counts from k0, set = kt % 2
-    const int buf = kt & (STAGES - 1);
-    const char* sb = sp_ + buf * OPB;
+    // DMA: a stage's DPS instructions go out in two halves, so that every run
+    // of MFMAs carries the same share: the first half of stage kt + D in the
+    // second half of step kt (its buffer is released by that step's barrier),
+    // the rest in the first half of step kt + 1.
+    // Registers: stage kt + 2 goes into LDS in the second half of step kt, and
+    // its set is loaded again with stage kt + 2 + RS, RS steps ahead of its
+    // use.
 #pragma unroll
-    for (int j = 0; j < FQ; ++j) M::go(fa[0], fb[j], acc[0][j]);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int st = 0; st < D; ++st)
+      if (st < steps) {
 #pragma unroll
-    for (int f = H; f < FP; ++f) fa[f] = fp.get(sb, f);
-    __builtin_amdgcn_sched_barrier(0);
-    constexpr int N1 = (H - 1) * FQ, D1 = DPS / 2, G1 = N1 / (D1 > 0 ? D1 : 1);
+        for (int q = 0; q < DPS; ++q)
+          if (st < D - 1 || q < DPS / 2) dma(q, st);
+      }
+    if constexpr (PIECES > 0) {
+      // stages 0 .. RS + 1 in flight together; everything has landed before
+      // the loop, so that the waits inside it only count the loop's own loads
+      typename RegP::Regs rp0[2];
+      typename RegQ::Regs rq0[2];
 #pragma unroll
-    for (int n = 0; n < N1; ++n) {
-      M::go(fa[1 + n / FQ], fb[n % FQ], acc[1 + n / FQ][n % FQ]);
-      if (D1 > 0 && n % G1 == G1 - 1 && n / G1 < D1) {
-        dma(D1 + n / G1, (kt + STAGES - 1) & (STAGES - 1), k0 + kt + STAGES - 1);
+      for (int st = 0; st < 2; ++st)
+        if (st < steps) fetch(Cut<true>(), rp0[st], rq0[st], st);
+#pragma unroll
+      for (int st = 0; st < RS; ++st)
+        if (2 + st < steps) fetch(Cut<true>(), rp[st], rq[st], 2 + st);
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+        if (st < steps) {
+#pragma unroll
+          for (int q = 0; q < PIECES; ++q) put(rp0[st], rq0[st], st, q);
+        }
+      __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
+    } else if (steps < D) {
+      __builtin_amdgcn_s_waitcnt(wait_imm(0, 15));
+    } else {
+      __builtin_amdgcn_s_waitcnt(wait_imm((D - 2) * DPS + DPS / 2, 15));
+    }
+    barrier();
+#pragma unroll
+    for (int f = 0; f < H; ++f) fa[f] = fp.get(sp_, f);
+#pragma unroll
+    for (int f = 0; f < FQ; ++f) fb0[f] = fq.get(sq_, f);
+
+    // A step, kt counting from k0, set = kt % RS.  Cut: near the end of the
+    // sum; what lies past it is not loaded.
+    auto step = [&](auto cut, int kt, int set, u32x4* fb, u32x4* fbn) {
+      constexpr bool CUT = decltype(cut)::value;
+      const char* sb = sp_ + (kt & (D - 1)) * OPB;
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) M::go(fa[0], fb[j], acc[0][j]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int f = H; f < FP; ++f) fa[f] = fp.get(sb, f);
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int N1 = (H - 1) * FQ, D1 = DPS / 2, G1 = N1 / (D1 > 0 ? D1 : 1);
+#pragma unroll
+      for (int n = 0; n < N1; ++n) {
+        M::go(fa[1 + n / FQ], fb[n % FQ], acc[1 + n / FQ][n % FQ]);
+        if (D1 > 0 && n % G1 == G1 - 1 && n / G1 < D1) {
+          if (!CUT || kt + D - 1 < steps) dma(D1 + n / G1, kt + D - 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      // This wave's DMAs of stage kt + 1 have landed ((D - 2) DPS later ones
+      // may fly; register loads among them make the wait stricter: counting
+      // them in measured 2-4 % slower on the weight gradients), its LDS
+      // writes of stage kt + 1 and its reads of stage kt are done.
+      if (CUT && DPS > 0 && kt + D - 1 >= steps) __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
+      else __builtin_amdgcn_s_waitcnt(wait_imm(DPS > 0 ? (D - 2) * DPS : 63, 0));
+      barrier();
+      const char *np_ = sp_ + ((kt + 1) & (D - 1)) * OPB, *nq_ = sq_ + ((kt + 1) & (D - 1)) * OPB;
+#pragma unroll
+      for (int f = 0; f < H; ++f) fa[f] = fp.get(np_, f);
+#pragma unroll
+      for (int f = 0; f < FQ; ++f) fbn[f] = fq.get(nq_, f);
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int N2 = H * FQ, G2 = N2 / (D1 > 0 ? D1 : 1);
+      constexpr int GP = PIECES > 0 ? N2 / (PIECES + 1) : N2;
+#pragma unroll
+      for (int n = 0; n < N2; ++n) {
+        M::go(fa[H + n / FQ], fb[n % FQ], acc[H + n / FQ][n % FQ]);
+        if (D1 > 0 && n % G2 == G2 - 1 && n / G2 < D1 && (!CUT || kt + D < steps)) dma(n / G2, kt + D);
+        if (PIECES > 0 && n % GP == GP - 1 && n / GP < PIECES) put(rp[set], rq[set], kt + 2, n / GP);
         __builtin_amdgcn_sched_barrier(0);
       }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    // This wave's DMAs of stage kt + 1 have landed (2 DPS later ones may fly;
-    // register loads among them make the wait stricter: counting them in
-    // measured 2-4 % slower on the weight gradients), its LDS writes of stage
-    // kt + 1 and its reads of stage kt are done.
-    __builtin_amdgcn_s_waitcnt(wait_imm(DPS > 0 ? 2 * DPS : 63, 0));
-    barrier();
-    const int nb = ((kt + 1) & (STAGES - 1)) * OPB;
-#pragma unroll
-    for (int f = 0; f < H; ++f) fa[f] = fp.get(sp_ + nb, f);
-#pragma unroll
-    for (int f = 0; f < FQ; ++f) fbn[f] = fq.get(sq_ + nb, f);
-    __builtin_amdgcn_sched_barrier(0);
-    constexpr int N2 = H * FQ, G2 = N2 / (D1 > 0 ? D1 : 1);
-    constexpr int PIECES = PIECES_ALL, GP = PIECES > 0 ? N2 / (PIECES + 1) : N2;
-#pragma unroll
-    for (int n = 0; n < N2; ++n) {
-      M::go(fa[H + n / FQ], fb[n % FQ], acc[H + n / FQ][n % FQ]);
-      if (D1 > 0 && n % G2 == G2 - 1 && n / G2 < D1) dma(n / G2, buf, k0 + kt + STAGES);
-      if (PIECES > 0 && n % GP == GP - 1 && n / GP < PIECES) put(set, (kt + 2) & (STAGES - 1), n / GP);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if constexpr (PIECES > 0) {
-      fetch(cut, set, k0 + kt + 2 + RS);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  const int steps = k1 - k0;
-  // Two steps per trip: the Q fragments and the register sets alternate
-  // without copies.  The trips whose register loads stay before the cut
-  // stages come first and carry no checks.
-  int kt = 0;
-  if constexpr (PIECES_ALL > 0) {
-    int safe = steps;
+      if constexpr (PIECES > 0) {
+        if (!CUT || kt + 2 + RS < steps) fetch(cut, rp[set], rq[set], kt + 2 + RS);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // Two steps per trip: the Q fragments and the register sets alternate
+    // without copies.  The trips whose loads stay before the end and the cut
+    // stages come first and carry no checks.
+    int kt = 0;
+    auto trips = [&](auto cut, int end) {
+      for (; kt + 1 < end; kt += 2) {
+        step(cut, kt, 0, fb0, fb1);
+        step(cut, kt + 1, 1, fb1, fb0);
+      }
+    };
+    int safe = steps - D;
     if constexpr (PREG) safe = min(safe, gp.safe - k0 - RS - 2);
     if constexpr (QREG) safe = min(safe, gq.safe - k0 - RS - 2);
-    for (; kt + 1 < safe; kt += 2) {
-      step(Cut<false>(), kt, 0, fb0, fb1);
-      step(Cut<false>(), kt + 1, 1, fb1, fb0);
-    }
+    trips(Cut<false>(), safe);
+    trips(Cut<true>(), steps);
+    if (kt < steps) step(Cut<true>(), kt, 0, fb0, fb1);
+    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));  // no load may land after the workgroup's LDS is given back
   }
-  for (; kt + 1 < steps; kt += 2) {
-    step(Cut<true>(), kt, 0, fb0, fb1);
-    step(Cut<true>(), kt + 1, 1, fb1, fb0);
-  }
-  if (kt < steps) step(Cut<true>(), kt, 0, fb0, fb1);
-  __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));  // no load may land after the workgroup's LDS is given back
 
   // acc[i][j][e] is column col0 + 16 i + 4 q4 + e of row row0 + 16 j + c16
   const int colt = wp * (T / 2) + 4 * q4, rowt = wq * (T / WQ) + c16;
@@ -620,10 +630,12 @@ __global__ void __launch_bounds__(256) few_kernel(const int8_t* xq, int64_t ldx,
     u32x4 a[PB], b[QB];
     const int left = k - whole * 64 - q4 * 16;
     auto part = [&](const int8_t* r, const int8_t* base, int64_t total) {
-      u32x4 v = {0, 0, 0, 0};
       const char* c = (const char*)r + whole * 64;
-      if (left >= 16) __builtin_memcpy(&v, c, 16);
-      else if (left > 0) v = load_part(c, left, (const char*)base, total);
+      if (total >= 16) return load_part(c, left, (const char*)base + total - 16);
+      u32x4 v = {0, 0, 0, 0};  // a matrix of less than 16 bytes
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < left) v[i / 4] |= (uint32_t)(uint8_t)c[i] << (8 * (i % 4));
       return v;
     };
 #pragma unroll
@@ -685,9 +697,10 @@ hipError_t go_mm(const MmParams& p, hipStream_t s) {
   const int64_t blocks = p.direct + rest * p.splits;
   if (blocks > 0x7fffffff || rest < 0 || (T == 256 && p.unaligned)) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)blocks);
-  if (T == 256) hipLaunchKernelGGL((mm_kernel<KIND, false, 256>), grid, dim3(512), 0, s, p);
-  else if (p.unaligned) hipLaunchKernelGGL((mm_kernel<KIND, true, 128>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((mm_kernel<KIND, false, 128>), grid, dim3(256), 0, s, p);
+  auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, p); };
+  if (T == 256) go(mm_kernel<KIND, false, 256>, 512);
+  else if (p.unaligned) go(mm_kernel<KIND, true, 128>, 256);
+  else go(mm_kernel<KIND, false, 128>, 256);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 sums((uint32_t)(T * T / 1024), (uint32_t)rest);
@@ -717,10 +730,9 @@ hipError_t launch_few(const int8_t* xq, int64_t ldx, const float* xs, const int8
   };
   // two blocks of w's rows per workgroup halve the reads of x; with fewer than
   // 256 workgroups left they would leave compute units without one
-  const bool two = n >= 256 * 32;
   if (t <= 16) return go(few_kernel<1, 1>, 16);
-  if (t <= 32) return two ? go(few_kernel<2, 2>, 32) : go(few_kernel<1, 2>, 16);
-  return two ? go(few_kernel<2, 4>, 32) : go(few_kernel<1, 4>, 16);
+  if (t > 32) return go(few_kernel<1, 4>, 16);
+  return n >= 256 * 32 ? go(few_kernel<2, 2>, 32) : go(few_kernel<1, 2>, 16);
 }
 
 hipError_t launch_pack(const void* src, int64_t lds, int64_t bytes, void* dst, int64_t ld, int64_t rows,
