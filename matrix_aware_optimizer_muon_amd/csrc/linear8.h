@@ -66,8 +66,9 @@ struct MmParams {
   int64_t ldp, ldq;         // bytes
   int padp, padq;           // bytes that may be read after the last row
   int np, nq, kd;           // output columns, output rows, contraction
-  int tile;                 // 256 or 128
-  bool unaligned;           // an operand that the DMA would read has rows off 16 bytes (tile 128)
+  int tile;                 // 256, 128 or 64
+  int groups;               // wave groups that share a tile's K: 1 or 2 (tile 128), 4 (tile 64)
+  bool unaligned;           // an operand that the DMA would read has rows off 16 bytes (not tile 256)
   int direct;               // tiles of one workgroup; the others are split
   int splits;               // contraction ranges of a split tile
   const float* sp;          // KIND_I8: per output column; else per row of P

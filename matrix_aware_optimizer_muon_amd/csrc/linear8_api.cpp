@@ -41,7 +41,7 @@ struct Choice {
   int64_t ldq = 0, ldp = 0;        // bytes, as the tile kernel reads them
   int padq = 0, padp = 0;          // readable after the last row
   int64_t at_q = 0, at_p = 0, at_part = 0;
-  int tile = 128, splits = 1, direct = 0;
+  int tile = 128, groups = 1, splits = 1, direct = 0;
   int np = 0, nq = 0, kd = 0;
   int64_t bytes = 0;
 };
@@ -68,7 +68,20 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
   const bool off_p = i8 && (!aligned(b, 16) || c.ldp % 16 || b_cols % 16);
   auto tiles = [&](int64_t T) { return (int64_t)((c.np + T - 1) / T) * ((c.nq + T - 1) / T); };
   const int64_t stages = (c.kd + (i8 ? 63 : 31)) / (i8 ? 64 : 32);
-  c.tile = tiles(256) >= 192 ? 256 : 128;
+  // Tiles by how many there are of them: 256-wide from three quarters of the
+  // compute units on; below, the smallest with at most one per unit, whose
+  // wave groups share K (groups), else 128-wide.  Measured (us, integer
+  // product of 300 x 2880 from 1408: 64-wide 6.6, 128 11.5; input gradient of
+  // 1024 x 3584 from 3584: 128 with two groups 39, one group 50, 256-wide 48).
+  if (tiles(256) >= 192) {
+    c.tile = 256;
+  } else if (tiles(64) <= 256) {
+    c.tile = 64;
+    c.groups = 4;
+  } else {
+    c.tile = 128;
+    c.groups = tiles(128) <= 256 ? 2 : 1;
+  }
   if (c.tile == 256) {
     c.pack_q = off_q;
     c.pack_p = off_p;
@@ -91,15 +104,24 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
     c.at_p = c.bytes;
     c.bytes += up(b_rows * c.ldp, 256);
   }
-  // Workgroups that run at once: whole rounds of them take a tile each, the
-  // tiles left over are split along K over one more round, unless the sum is
-  // too short to pay for the second launch (about 4 us).  128-wide tiles run
-  // two to a compute unit.
+  // Workgroups that run at once: whole rounds of them take a tile each; the
+  // tiles left over may be split along K over one more round.  A split costs a
+  // second launch (4 us) and its partial sums' way to memory and back (at 4
+  // TB/s), and saves a part of the stages: 0.3 us each for the integer
+  // product's small tiles, 0.55 us for the gradients', 1 us for 256-wide ones
+  // (measured).  So a weight gradient of 512 x 3584 from 4096 tokens is split
+  // (33 against 43 us), a product of 4096 x 512 from 3584 is not (18 against
+  // 26).  128-wide tiles of one group run two to a compute unit.
   const int64_t all = tiles(c.tile);
-  const int64_t slots = c.tile == 256 ? 256 : 512, rest = all % slots;
+  const int64_t slots = c.tile == 128 && c.groups == 1 ? 512 : 256, rest = all % slots;
+  const int64_t each = stages / c.groups;  // a group's stages
   c.direct = (int)all;
-  if (rest > 0 && stages >= 24) {
-    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({slots / rest, stages / 8, 32}));
+  if (rest > 0) {
+    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({slots / rest, each / 4, 32}));
+    const double tile_us = (double)c.tile * c.tile * 8 / 4e6;  // written and read
+    const double stage_us = c.tile == 256 ? 1.0 : i8 ? 0.3 : 0.55;
+    const double saved = stage_us * (double)(each - each / c.splits), cost = 4.0 + tile_us * (double)(rest * c.splits);
+    if (saved < cost) c.splits = 1;
     if (c.splits > 1) {
       c.direct = (int)(all - rest);
       c.at_part = c.bytes;
@@ -153,6 +175,7 @@ muon_status run_product(muon_q8_product kind, const void* a, int64_t lda, const 
   p.nq = c.nq;
   p.kd = c.kd;
   p.tile = c.tile;
+  p.groups = c.groups;
   p.unaligned = c.unaligned;
   p.direct = c.direct;
   p.splits = c.splits;

@@ -12,8 +12,9 @@
 // widened copy exists in memory.  2.5 vector instructions per element, once
 // per workgroup, run between the MFMAs.
 //
-// Tiles: 256 x 256 (8 waves, 2 x 4, each 128 x 64) or 128 x 128 (4 waves,
-// 2 x 2, each 64 x 64).  A stage is 64 bytes of K per operand row (64 int8,
+// Tiles: 256 x 256 (8 waves, 2 x 4, each 128 x 64), 128 x 128 (one or two
+// groups of 4 waves, 2 x 2, each 64 x 64) or 64 x 64 (four groups of 4 waves,
+// each 32 x 32).  A stage is 64 bytes of K per operand row (64 int8,
 // 32 bf16): one MFMA K step.  Stages stream through a four-deep LDS
 // ring filled by direct global->LDS loads or from registers; one barrier per stage, placed so that it
 // publishes the next stage and retires the reads of the current one, and a
@@ -50,9 +51,14 @@ __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory
 // 16-byte chunk swizzles.  A K-contiguous row has 4 chunks: bit 1 flips with
 // row bit 2 (fragment reads of 16 rows x 4 chunks are conflict free).  A
 // K-major row has 16 or 32: an even XOR from row bits 0, 1 and 3, so the 16
-// rows of 32 bytes that a transposing read takes fall on eight pair places.
+// rows of 32 bytes that a transposing read takes (bit 2 is fixed) fall on
+// eight pair places; with 8 chunks (64 columns) row bit 0 is the upper half
+// of the banks already, and bits 1 and 3 make four pair places.
 __device__ __forceinline__ int swz_c(int row) { return ((row >> 2) & 1) << 1; }
-__device__ __forceinline__ int swz_k(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) << 1; }
+template <int T>
+__device__ __forceinline__ int swz_k(int k) {
+  return T == 64 ? ((k >> 1) & 1) << 1 | ((k >> 3) & 1) << 2 : ((k & 3) | (((k >> 3) & 1) << 2)) << 1;
+}
 
 __device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -96,7 +102,7 @@ struct DmaOperand {
       if constexpr (KM) {
         constexpr int RB = T * 2, RPI = 1024 / RB, CH = RB / 16;
         const int k = (wave * NDMA + i) * RPI + lane / CH;
-        const int ch = (lane % CH) ^ swz_k(k);
+        const int ch = (lane % CH) ^ swz_k<T>(k);
         const int c = min(row0 + ch * 8, (count - 1) & ~7);  // whole chunks, in the padded row
         in = full * KROWS + k < kd;
         // where there is no whole stage, `src` is never read
@@ -122,39 +128,41 @@ struct DmaOperand {
   }
 };
 
-// The bytes [0, n) at a (none: n <= 0, all: n >= 16), zeros beyond.  last: the
-// last place of the matrix where 16 bytes can be read; the bytes wanted lie
-// before its end.  One read at any address, shifted and masked into place,
-// without a branch: byte reads behind their predicates took 8 us of a
-// one-stage product.
+// The first n bytes wanted of a 16-byte read (8 bytes: the low half) that was
+// moved back by d bytes to stay inside its matrix, zeros beyond (none: n <= 0).
+__device__ __forceinline__ u32x4 put_in_place(u32x4 v, int d, int n) {
+  uint64_t w0 = (uint64_t)v[1] << 32 | v[0], w1 = (uint64_t)v[3] << 32 | v[2];
+  const int sh = (d & 7) * 8;
+  w0 = d & 8 ? w1 : w0;
+  w1 = d & 8 ? 0 : w1;
+  w0 = sh ? (w0 >> sh) | (w1 << (64 - sh)) : w0;
+  w1 >>= sh;
+  const uint64_t m = (1ull << ((n & 7) * 8)) - 1;  // the cut half's bytes
+  w0 &= n >= 8 ? ~0ull : n > 0 ? m : 0ull;
+  w1 &= n >= 16 ? ~0ull : n > 8 ? m : 0ull;
+  return u32x4{(uint32_t)w0, (uint32_t)(w0 >> 32), (uint32_t)w1, (uint32_t)(w1 >> 32)};
+}
+// last: the last place of the matrix where 16 bytes can be read.
 __device__ __forceinline__ u32x4 load_part(const char* a, int n, const char* last) {
   const char* at = a < last ? a : last;
-  const int d = (int)(a - at) & 15;  // (over 15 only where n <= 0)
-  uint64_t w[2];
-  __builtin_memcpy(w, at, 16);
-  const int sh = (d & 7) * 8;
-  if (d & 8) {
-    w[0] = w[1];
-    w[1] = 0;
-  }
-  w[0] = sh ? (w[0] >> sh) | (w[1] << (64 - sh)) : w[0];
-  w[1] >>= sh;
-  const uint64_t m = (1ull << ((n & 7) * 8)) - 1;  // the cut half's bytes
-  w[0] &= n >= 8 ? ~0ull : n > 0 ? m : 0ull;
-  w[1] &= n >= 16 ? ~0ull : n > 8 ? m : 0ull;
-  return u32x4{(uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32)};
+  u32x4 v;
+  __builtin_memcpy(&v, at, 16);
+  return put_in_place(v, (int)(a - at) & 15, n);  // (over 15 only where n <= 0)
 }
 
-// One operand fed through registers, 16 bytes of a row per lane and chunk:
-// at any address, and, with CONV, int8 rows times their scale widened to
-// bf16 on the way (16 values per lane, two 16-byte LDS writes).  Whole 16-byte
-// reads that leave the row stay inside the matrix for all stages before
-// `safe` (load); load_cut, for any stage, reads what exists and takes zero for
-// the rest.  The matrix has at least 16 bytes (`pad` of them may follow its
-// last row).
+// One operand fed through registers, CH bytes of a row per lane and chunk: at
+// any address, and, with CONV, int8 rows times their scale widened to bf16 on
+// the way.  Whole reads that leave the row stay inside the matrix for all
+// stages before `safe` (load).  load_cut, for any stage, moves a read that
+// would leave the matrix back inside, and `store` puts such bytes in place and
+// zeros what lies past the row or the sum: without a branch, and only when the
+// stage is due, so that loads stay in flight (byte reads behind their
+// predicates took 8 us of a one-stage product).  The matrix has at least 16
+// bytes (`pad` of them may follow its last row).
 template <bool KM, bool CONV, int T, int NT>
 struct RegOperand {
-  static constexpr int CPR = KM ? (CONV ? T / 16 : T / 8) : 4;   // chunks per stage row
+  static constexpr int CH = CONV && T == 64 ? 8 : 16;
+  static constexpr int CPR = KM ? (CONV ? T : T * 2) / CH : 4;   // chunks per stage row
   static constexpr int SROWS = KM ? KROWS : T;                   // stage rows
   static constexpr int N = SROWS * CPR / NT;                     // chunks per lane
   static_assert(N * NT == SROWS * CPR && (!CONV || N == 1), "whole chunks per lane");
@@ -171,7 +179,7 @@ struct RegOperand {
 
   __device__ __forceinline__ void init(const char* base, int64_t ld, int pad, const float* sc, int row0,
                                        int count, int kdim, int kbytes, int full, int tid) {
-    last = base - 16 + pad +
+    last = base - CH + pad +
            (KM ? (int64_t)(kdim - 1) * ld + count * (CONV ? 1 : 2) : (int64_t)(count - 1) * ld + kbytes);
     row = tid / CPR;
     col = tid % CPR;
@@ -179,12 +187,12 @@ struct RegOperand {
     scale = sc;
     if constexpr (KM) {
       constexpr int SZ = CONV ? 1 : 2;
-      const int rb = count * SZ, last = (rb - 1) & ~15;  // row bytes, its last chunk
-      const int c = min(row0 * SZ + col * 16, last);
+      const int rb = count * SZ, end = (rb - 1) & ~(CH - 1);  // row bytes, its last chunk
+      const int c = min(row0 * SZ + col * CH, end);
       left = rb - c;
       step = KROWS * ld;
       // rows whose last chunk, read whole, ends inside the matrix
-      const int over = last + 16 - rb;
+      const int over = end + CH - rb;
       const int64_t rows = over > 0 ? kd - (over + ld - 1) / ld : kd;
       safe = rows > 0 ? (int)(rows / KROWS) : 0;
 #pragma unroll
@@ -192,39 +200,45 @@ struct RegOperand {
     } else {
       step = KB;
       safe = full;
-      left = kbytes - col * 16;
+      left = kbytes - col * CH;
 #pragma unroll
-      for (int i = 0; i < N; ++i) src[i] = base + (int64_t)min(row0 + row + i * (T / N), count - 1) * ld + col * 16;
+      for (int i = 0; i < N; ++i) src[i] = base + (int64_t)min(row0 + row + i * (T / N), count - 1) * ld + col * CH;
     }
   }
   // A stage before `safe`.
   __device__ __forceinline__ void load(Regs& r, int ks) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) __builtin_memcpy(&r.v[i], src[i] + ks * step, 16);
+    for (int i = 0; i < N; ++i) __builtin_memcpy(&r.v[i], src[i] + ks * step, CH);
     if constexpr (CONV) r.scale = scale[ks * KROWS + row];
   }
   // Any stage.
   __device__ __forceinline__ void load_cut(Regs& r, int ks) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      int n;
-      if constexpr (KM) n = ks * KROWS + row + i * (KROWS / N) < kd ? left : 0;
-      else n = left - ks * KB;
-      r.v[i] = load_part(src[i] + ks * step, n, last);
+      const char* a = src[i] + ks * step;
+      __builtin_memcpy(&r.v[i], a < last ? a : last, CH);
     }
-    if constexpr (CONV) {
-      const int k = ks * KROWS + row;
-      const float f = scale[min(k, kd - 1)];
-      r.scale = k < kd ? f : 0.0f;
-    }
+    if constexpr (CONV) r.scale = scale[min(ks * KROWS + row, kd - 1)];
+  }
+  // Chunk i of a stage that load_cut (or load) has read.
+  __device__ __forceinline__ void mend(Regs& r, int i, int ks) const {
+    const char* a = src[i] + ks * step;
+    const int d = a < last ? 0 : (int)(a - last) & (CH - 1);
+    int n;
+    if constexpr (KM) n = ks * KROWS + row + i * (KROWS / N) < kd ? left : 0;
+    else n = left - ks * KB;
+    r.v[i] = put_in_place(r.v[i], d, n);
+    if constexpr (CONV) r.scale = ks * KROWS + row < kd ? r.scale : 0.0f;
   }
   // Piece q of PIECES of a stage's way into LDS, so that the caller can put
   // MFMAs between them.
-  static constexpr int PIECES = CONV ? 4 : N;
+  static constexpr int PIECES = CONV ? CH / 4 : N;
   struct Wide {
-    u32x4 lo, hi;
+    uint32_t d[CONV ? CH / 2 : 1];
   };
-  __device__ __forceinline__ void store(const Regs& r, Wide& w, char* stage, int q) const {
+  template <bool CUT>
+  __device__ __forceinline__ void store(Regs& r, Wide& w, char* lds, int stage, int ks, int q) const {
+    if (CUT && (!CONV || q == 0)) mend(r, q, ks);
     if constexpr (CONV) {
       // (opaque: the compiler otherwise takes the bytes apart at the load,
       // carries 16 registers for 4 and waits for the load to do so)
@@ -233,26 +247,20 @@ struct RegOperand {
       float f[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(b >> (8 * e)) * r.scale;
-      const uint32_t d0 = pack_bf16(f[0], f[1]), d1 = pack_bf16(f[2], f[3]);
-      if (q < 2) {
-        w.lo[2 * q] = d0;
-        w.lo[2 * q + 1] = d1;
-      } else {
-        w.hi[2 * q - 4] = d0;
-        w.hi[2 * q - 3] = d1;
-      }
-      if (q == 3) {
-        // swz_k is even, so the lane's two chunks stay side by side
-        char* d = stage + row * (T * 2) + (((2 * col) ^ swz_k(row)) << 4);
-        *(u32x4*)d = w.lo;
-        *(u32x4*)(d + 16) = w.hi;
+      w.d[2 * q] = pack_bf16(f[0], f[1]);
+      w.d[2 * q + 1] = pack_bf16(f[2], f[3]);
+      if (q == PIECES - 1) {
+        // swz_k is even, so a lane's two chunks stay side by side
+        const int d = stage + row * (T * 2) + ((col * (CH / 8) ^ swz_k<T>(row)) << 4);
+        *(u32x4*)(lds + d) = u32x4{w.d[0], w.d[1], w.d[2], w.d[3]};
+        if constexpr (CH == 16) *(u32x4*)(lds + d + 16) = u32x4{w.d[4], w.d[5], w.d[6], w.d[7]};
       }
     } else if constexpr (KM) {
       const int k = row + q * (KROWS / N);
-      *(u32x4*)(stage + k * (T * 2) + ((col ^ swz_k(k)) << 4)) = r.v[q];
+      *(u32x4*)(lds + (stage + k * (T * 2) + ((col ^ swz_k<T>(k)) << 4))) = r.v[q];
     } else {
       const int t = row + q * (T / N);
-      *(u32x4*)(stage + t * KB + ((col ^ swz_c(t)) << 4)) = r.v[q];
+      *(u32x4*)(lds + (stage + t * KB + ((col ^ swz_c(t)) << 4))) = r.v[q];
     }
   }
 };
@@ -261,27 +269,31 @@ struct RegOperand {
 template <bool KM, int T>
 struct Reader {
   int off, sw, col;
-  __device__ __forceinline__ void init(int first, int q4, int c16) {
+  __device__ __forceinline__ void init(int ring, int first, int q4, int c16) {
     if constexpr (KM) {
       // two transposing reads, k 8 q4 .. +3 and +4 .. +7 (swz_k equal: bit 2
       // does not enter it); the lane addresses row 8 q4 + c16 / 4 (+ 4) and
       // columns first + 16 f + 4 (c16 % 4) .. +3
       const int k = 8 * q4 + (c16 >> 2);
       off = k * T * 2 + ((c16 & 3) >> 1) * 16 + (c16 & 1) * 8;
-      sw = swz_k(k) << 4;
+      sw = swz_k<T>(k) << 4;
       col = first >> 3;
     } else {
       const int r = first + c16;
       off = r * KB + ((q4 ^ swz_c(r)) << 4);
     }
+    off += ring;
+    asm("" : "+v"(off));  // (see get: keeps `ring` from becoming a base of its own)
   }
-  __device__ __forceinline__ u32x4 get(const char* stage, int f) const {
+  // (one addition to the LDS object's address: through a longer chain the
+  // compiler loses which object is read, and waits for every DMA)
+  __device__ __forceinline__ u32x4 get(const char* lds, int stage, int f) const {
     if constexpr (KM) {
-      const char* a = stage + off + (((col + 2 * f) << 4) ^ sw);
-      const uint2 lo = tr_read(a), hi = tr_read(a + 4 * T * 2);
+      const int a = stage + off + (((col + 2 * f) << 4) ^ sw);
+      const uint2 lo = tr_read(lds + a), hi = tr_read(lds + a + 4 * T * 2);
       return u32x4{lo.x, lo.y, hi.x, hi.y};
     } else {
-      return *(const u32x4*)(stage + off + f * 16 * KB);
+      return *(const u32x4*)(lds + (stage + off + f * 16 * KB));
     }
   }
 };
@@ -322,13 +334,22 @@ template <bool C> struct Cut { static constexpr bool value = C; };
 // How the kernel reads its operands: P through registers for the gradients
 // (widened), by DMA or, at unaligned addresses, through registers for the
 // integer product; Q by DMA or, unaligned, through registers.
-template <int KIND, bool UNALIGNED, int T>
-__global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_kernel(const MmParams p) {
+//
+// G groups of waves share a tile, each with a share of K and LDS rings of its
+// own, and join their sums through LDS: where there are no more tiles than
+// compute units, a group alone on its SIMDs waits for LDS and barriers most of
+// the time (0.37 us per stage of a 128 x 128 tile, a third of it MFMAs), and
+// the join costs no second launch.
+constexpr int waves_of(int T) { return T == 256 ? 8 : 4; }
+
+template <int KIND, bool UNALIGNED, int T, int G>
+__global__ void __launch_bounds__(64 * waves_of(T) * G, T == 128 && G == 1 ? 2 : 1)
+    mm_kernel(const MmParams p) {
   constexpr bool I8K = KIND == KIND_I8, PKM = !I8K, QKM = KIND == KIND_DW;
   constexpr bool PREG = !I8K || UNALIGNED, QREG = UNALIGNED;
   typedef Mfma<I8K> M;
   typedef typename M::Acc Acc;
-  constexpr int NW = T == 256 ? 8 : 4;
+  constexpr int NW = waves_of(T);                // waves of a group
   constexpr int WQ = NW / 2;                     // waves along Q (2 along P)
   constexpr int FP = T / 2 / 16, FQ = T / WQ / 16;  // 16 x 16 blocks per wave
   constexpr int H = FP / 2;                      // block rows per half stage
@@ -337,16 +358,20 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
   typedef RegOperand<PKM, PKM, T, 64 * NW> RegP;
   typedef RegOperand<QKM, false, T, 64 * NW> RegQ;
   constexpr int DP = PREG ? 0 : DmaP::NDMA, DPS = DP + (QREG ? 0 : DmaQ::NDMA);
+  constexpr int DB = DPS / 2, DA = DPS - DB;     // the two halves of a stage's instructions
   constexpr int OPB = T * KB;                    // one operand's stage in LDS
   constexpr int D = 4;                           // stages of a ring
   constexpr int RS = 2;                          // register sets in flight
   // (two objects: the compiler then knows that a write to one is no write to
   // the other)
-  __shared__ __attribute__((aligned(1024))) char sp_[D * OPB];
-  __shared__ __attribute__((aligned(1024))) char sq_[D * OPB];
+  __shared__ __attribute__((aligned(1024))) char s_p[G * D * OPB];
+  __shared__ __attribute__((aligned(1024))) char s_q[G * D * OPB];
 
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x % (64 * NW), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = G > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / (64 * NW)) : 0;
+  const int ring = group * D * OPB;              // the group's rings
+  auto at = [&](int st) { return (st & (D - 1)) * OPB; };  // a stage in them
   const int wp = wave / WQ, wq = wave % WQ;
   const int q4 = lane >> 4, c16 = lane & 15;
 
@@ -373,7 +398,10 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
     k0 = (int)((int64_t)nk * split / splits);
     k1 = (int)((int64_t)nk * (split + 1) / splits);
   }
-  const int steps = k1 - k0;
+  // stages per group, and this group's (the last ones may have fewer)
+  const int most = (k1 - k0 + G - 1) / G;
+  const int steps = G > 1 ? max(0, min(most, k1 - k0 - group * most)) : most;
+  k0 += group * most;
   const int kbytes = p.kd * (I8K ? 1 : 2);
 
   Acc acc[FP][FQ];
@@ -391,15 +419,15 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
     else dp.init(p.P, p.ldp, tp * T, p.np, p.kd, kbytes, full, tid);
     if constexpr (QREG) gq.init(p.Q, p.ldq, p.padq, nullptr, tq * T, p.nq, p.kd, kbytes, full, tid);
     else dq.init(p.Q, p.ldq, tq * T, p.nq, p.kd, kbytes, full, tid);
-    auto dma = [&](int q, int st) {  // instruction q of stage k0 + st
-      if (q < DP) dp.load(q, sp_ + (st & (D - 1)) * OPB, k0 + st, full, wave);
-      else dq.load(q - DP, sq_ + (st & (D - 1)) * OPB, k0 + st, full, wave);
+    auto dma = [&](int q, int st) __attribute__((always_inline)) {  // instruction q of stage k0 + st
+      if (q < DP) dp.load(q, s_p + ring + at(st), k0 + st, full, wave);
+      else dq.load(q - DP, s_q + ring + at(st), k0 + st, full, wave);
     };
     typename RegP::Regs rp[RS];
     typename RegQ::Regs rq[RS];
     typename RegP::Wide wp8;
     typename RegQ::Wide wq8;
-    auto fetch = [&](auto cut, typename RegP::Regs& a, typename RegQ::Regs& b, int st) {
+    auto fetch = [&](auto cut, typename RegP::Regs& a, typename RegQ::Regs& b, int st) __attribute__((always_inline)) {
       if constexpr (PREG) {
         if constexpr (decltype(cut)::value) gp.load_cut(a, k0 + st);
         else gp.load(a, k0 + st);
@@ -409,16 +437,18 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
         else gq.load(b, k0 + st);
       }
     };
-    // pieces of a register set's way into LDS
+    // pieces of a register set's way into LDS as stage k0 + st
     constexpr int PP = PREG ? RegP::PIECES : 0, PQ = QREG ? RegQ::PIECES : 0, PIECES = PP + PQ;
-    auto put = [&](const typename RegP::Regs& a, const typename RegQ::Regs& b, int st, int q) {
-      if (q < PP) gp.store(a, wp8, sp_ + (st & (D - 1)) * OPB, q);
-      else if (q < PIECES) gq.store(b, wq8, sq_ + (st & (D - 1)) * OPB, q - PP);
+    auto put = [&](auto cut, typename RegP::Regs& a, typename RegQ::Regs& b, int st,
+                   int q) __attribute__((always_inline)) {
+      constexpr bool CUT = decltype(cut)::value;
+      if (q < PP) gp.template store<CUT>(a, wp8, s_p, ring + at(st), k0 + st, q);
+      else if (q < PIECES) gq.template store<CUT>(b, wq8, s_q, ring + at(st), k0 + st, q - PP);
     };
     Reader<PKM, T> fp;
     Reader<QKM, T> fq;
-    fp.init(wp * (T / 2), q4, c16);
-    fq.init(wq * (T / WQ), q4, c16);
+    fp.init(ring, wp * (T / 2), q4, c16);
+    fq.init(ring, wq * (T / WQ), q4, c16);
     u32x4 fa[FP], fb0[FQ], fb1[FQ];
 
     // DMA: a stage's DPS instructions go out in two halves, so that every run
@@ -433,7 +463,7 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
       if (st < steps) {
 #pragma unroll
         for (int q = 0; q < DPS; ++q)
-          if (st < D - 1 || q < DPS / 2) dma(q, st);
+          if (st < D - 1 || q < DA) dma(q, st);
       }
     if constexpr (PIECES > 0) {
       // stages 0 .. RS + 1 in flight together; everything has landed before
@@ -441,48 +471,48 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
       typename RegP::Regs rp0[2];
       typename RegQ::Regs rq0[2];
 #pragma unroll
-      for (int st = 0; st < 2; ++st)
-        if (st < steps) fetch(Cut<true>(), rp0[st], rq0[st], st);
+      for (int st = 0; st < 2; ++st) fetch(Cut<true>(), rp0[st], rq0[st], st);
 #pragma unroll
-      for (int st = 0; st < RS; ++st)
-        if (2 + st < steps) fetch(Cut<true>(), rp[st], rq[st], 2 + st);
+      for (int st = 0; st < RS; ++st) fetch(Cut<true>(), rp[st], rq[st], 2 + st);
 #pragma unroll
       for (int st = 0; st < 2; ++st)
-        if (st < steps) {
 #pragma unroll
-          for (int q = 0; q < PIECES; ++q) put(rp0[st], rq0[st], st, q);
-        }
+        for (int q = 0; q < PIECES; ++q) put(Cut<true>(), rp0[st], rq0[st], st, q);
       __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
     } else if (steps < D) {
       __builtin_amdgcn_s_waitcnt(wait_imm(0, 15));
     } else {
-      __builtin_amdgcn_s_waitcnt(wait_imm((D - 2) * DPS + DPS / 2, 15));
+      __builtin_amdgcn_s_waitcnt(wait_imm((D - 2) * DPS + DA, 15));
     }
     barrier();
 #pragma unroll
-    for (int f = 0; f < H; ++f) fa[f] = fp.get(sp_, f);
+    for (int f = 0; f < H; ++f) fa[f] = fp.get(s_p, at(0), f);
 #pragma unroll
-    for (int f = 0; f < FQ; ++f) fb0[f] = fq.get(sq_, f);
+    for (int f = 0; f < FQ; ++f) fb0[f] = fq.get(s_q, at(0), f);
 
     // A step, kt counting from k0, set = kt % RS.  Cut: near the end of the
     // sum; what lies past it is not loaded.
-    auto step = [&](auto cut, int kt, int set, u32x4* fb, u32x4* fbn) {
+    auto step = [&](auto cut, int kt, int set, u32x4* fb, u32x4* fbn) __attribute__((always_inline)) {
       constexpr bool CUT = decltype(cut)::value;
-      const char* sb = sp_ + (kt & (D - 1)) * OPB;
 #pragma unroll
       for (int j = 0; j < FQ; ++j) M::go(fa[0], fb[j], acc[0][j]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int f = H; f < FP; ++f) fa[f] = fp.get(sb, f);
+      for (int f = H; f < FP; ++f) fa[f] = fp.get(s_p, at(kt), f);
       __builtin_amdgcn_sched_barrier(0);
-      constexpr int N1 = (H - 1) * FQ, D1 = DPS / 2, G1 = N1 / (D1 > 0 ? D1 : 1);
+      constexpr int N1 = (H - 1) * FQ, G1 = DB > 0 && N1 > DB ? N1 / (DB + (DB == 0)) : 1;
 #pragma unroll
       for (int n = 0; n < N1; ++n) {
         M::go(fa[1 + n / FQ], fb[n % FQ], acc[1 + n / FQ][n % FQ]);
-        if (D1 > 0 && n % G1 == G1 - 1 && n / G1 < D1) {
-          if (!CUT || kt + D - 1 < steps) dma(D1 + n / G1, kt + D - 1);
+        if (DB > 0 && n % G1 == G1 - 1 && n / G1 < DB) {
+          if (!CUT || kt + D - 1 < steps) dma(DA + n / G1, kt + D - 1);
           __builtin_amdgcn_sched_barrier(0);
         }
+      }
+      if constexpr (N1 == 0) {
+#pragma unroll
+        for (int q = 0; q < DB; ++q)
+          if (!CUT || kt + D - 1 < steps) dma(DA + q, kt + D - 1);
       }
       __builtin_amdgcn_sched_barrier(0);
       // This wave's DMAs of stage kt + 1 have landed ((D - 2) DPS later ones
@@ -492,19 +522,23 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
       if (CUT && DPS > 0 && kt + D - 1 >= steps) __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
       else __builtin_amdgcn_s_waitcnt(wait_imm(DPS > 0 ? (D - 2) * DPS : 63, 0));
       barrier();
-      const char *np_ = sp_ + ((kt + 1) & (D - 1)) * OPB, *nq_ = sq_ + ((kt + 1) & (D - 1)) * OPB;
 #pragma unroll
-      for (int f = 0; f < H; ++f) fa[f] = fp.get(np_, f);
+      for (int f = 0; f < H; ++f) fa[f] = fp.get(s_p, at(kt + 1), f);
 #pragma unroll
-      for (int f = 0; f < FQ; ++f) fbn[f] = fq.get(nq_, f);
+      for (int f = 0; f < FQ; ++f) fbn[f] = fq.get(s_q, at(kt + 1), f);
       __builtin_amdgcn_sched_barrier(0);
-      constexpr int N2 = H * FQ, G2 = N2 / (D1 > 0 ? D1 : 1);
-      constexpr int GP = PIECES > 0 ? N2 / (PIECES + 1) : N2;
+      constexpr int N2 = H * FQ, G2 = N2 / (DA > 0 ? DA : 1);
+      // pieces after each MFMA (several, where there are few MFMAs)
+      constexpr int GP = N2 > PIECES ? N2 / (PIECES + 1) : 1, PB = (PIECES + N2 - 1) / N2;
 #pragma unroll
       for (int n = 0; n < N2; ++n) {
         M::go(fa[H + n / FQ], fb[n % FQ], acc[H + n / FQ][n % FQ]);
-        if (D1 > 0 && n % G2 == G2 - 1 && n / G2 < D1 && (!CUT || kt + D < steps)) dma(n / G2, kt + D);
-        if (PIECES > 0 && n % GP == GP - 1 && n / GP < PIECES) put(rp[set], rq[set], kt + 2, n / GP);
+        if (DA > 0 && n % G2 == G2 - 1 && n / G2 < DA && (!CUT || kt + D < steps)) dma(n / G2, kt + D);
+        if (PIECES > 0 && n % GP == GP - 1) {
+#pragma unroll
+          for (int q = 0; q < PB; ++q)
+            if (n / GP * PB + q < PIECES) put(cut, rp[set], rq[set], kt + 2, n / GP * PB + q);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (PIECES > 0) {
@@ -516,7 +550,7 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
     // without copies.  The trips whose loads stay before the end and the cut
     // stages come first and carry no checks.
     int kt = 0;
-    auto trips = [&](auto cut, int end) {
+    auto trips = [&](auto cut, int end) __attribute__((always_inline)) {
       for (; kt + 1 < end; kt += 2) {
         step(cut, kt, 0, fb0, fb1);
         step(cut, kt + 1, 1, fb1, fb0);
@@ -530,6 +564,33 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
     if (kt < steps) step(Cut<true>(), kt, 0, fb0, fb1);
     __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));  // no load may land after the workgroup's LDS is given back
   }
+  if constexpr (G > 1) {
+    // a group's barriers: one ahead of the loop and one per step; then one
+    // that ends all reads of the rings
+    if (most > 0) {
+      for (int i = steps > 0 ? steps : -1; i < most; ++i) barrier();
+    }
+    barrier();
+    // Block b of every wave is finished by group b % G: the other groups
+    // leave theirs in LDS, lane by lane, and it adds them in their order.
+    constexpr int B = FP * FQ;
+    static_assert(B % G == 0 && B * (G - 1) * NW * 1024 <= G * D * OPB, "the join fits the ring");
+    auto slot = [&](int b, int from) -> Acc* {
+      const int o = b % G;
+      return (Acc*)(s_p + (((b / G) * G + o) * (G - 1) + (from < o ? from : from - 1)) * (NW * 1024) + tid * 16);
+    };
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (b % G != group) *slot(b, group) = acc[b / FQ][b % FQ];
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (b % G == group) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          if (g != b % G) acc[b / FQ][b % FQ] += *slot(b, g);
+      }
+  }
 
   // acc[i][j][e] is column col0 + 16 i + 4 q4 + e of row row0 + 16 j + c16
   const int colt = wp * (T / 2) + 4 * q4, rowt = wq * (T / WQ) + c16;
@@ -538,7 +599,8 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
 #pragma unroll
     for (int j = 0; j < FQ; ++j)
 #pragma unroll
-      for (int i = 0; i < FP; ++i) *(Acc*)(part + (rowt + 16 * j) * T + colt + 16 * i) = acc[i][j];
+      for (int i = 0; i < FP; ++i)
+        if (G == 1 || (i * FQ + j) % G == group) *(Acc*)(part + (rowt + 16 * j) * T + colt + 16 * i) = acc[i][j];
     return;
   }
   const int col0 = tp * T + colt, row0 = tq * T + rowt;
@@ -552,7 +614,7 @@ __global__ void __launch_bounds__(T == 256 ? 512 : 256, T == 256 ? 1 : 2) mm_ker
     for (int i = 0; i < FP; ++i) {
       const int c = col0 + 16 * i;
       const int n = p.np - c;
-      if (n <= 0) continue;
+      if (n <= 0 || (G > 1 && (i * FQ + j) % G != group)) continue;
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -697,16 +759,18 @@ hipError_t go_mm(const MmParams& p, hipStream_t s) {
   const int64_t blocks = p.direct + rest * p.splits;
   if (blocks > 0x7fffffff || rest < 0 || (T == 256 && p.unaligned)) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)blocks);
-  auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, p); };
-  if (T == 256) go(mm_kernel<KIND, false, 256>, 512);
-  else if (p.unaligned) go(mm_kernel<KIND, true, 128>, 256);
-  else go(mm_kernel<KIND, false, 128>, 256);
+  auto go = [&](auto kernel, int waves) { hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, s, p); };
+  if (T == 256) go(mm_kernel<KIND, false, 256, 1>, 8);
+  else if (T == 128 && p.groups == 2) p.unaligned ? go(mm_kernel<KIND, true, 128, 2>, 8) : go(mm_kernel<KIND, false, 128, 2>, 8);
+  else if (T == 128) p.unaligned ? go(mm_kernel<KIND, true, 128, 1>, 4) : go(mm_kernel<KIND, false, 128, 1>, 4);
+  else p.unaligned ? go(mm_kernel<KIND, true, 64, 4>, 16) : go(mm_kernel<KIND, false, 64, 4>, 16);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 sums((uint32_t)(T * T / 1024), (uint32_t)rest);
   constexpr bool I8K = KIND == KIND_I8;
   if (T == 256) hipLaunchKernelGGL((mm_sum_kernel<I8K, 256>), sums, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((mm_sum_kernel<I8K, 128>), sums, dim3(256), 0, s, p);
+  else if (T == 128) hipLaunchKernelGGL((mm_sum_kernel<I8K, 128>), sums, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((mm_sum_kernel<I8K, 64>), sums, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
