@@ -45,7 +45,7 @@ struct NormBackParams {
 hipError_t launch_norm(const NormParams& p, bool bf16, hipStream_t s);
 hipError_t launch_norm_back(const NormBackParams& p, bool bf16, hipStream_t s);
 hipError_t launch_norm_back_sum(const float* part, float* dw, int groups, int64_t cols, hipStream_t s);
-int norm_back_groups(int64_t rows, int64_t cols);
+int norm_back_groups(int64_t rows, int64_t cols, bool bf16);  // never more for fp32
 hipError_t launch_quantize(const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
                            int64_t rows, int64_t cols, bool bf16, hipStream_t s);
 hipError_t launch_dequantize(const int8_t* q, int64_t ldq, const float* scale, void* x, int64_t ldx,

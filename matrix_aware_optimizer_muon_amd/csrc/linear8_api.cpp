@@ -241,7 +241,7 @@ muon_status muon_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t* 
   const muon_status bad = row_sizes(rows, cols);
   if (bad != MUON_OK) return bad;
   if (!workspace_bytes) return MUON_ERR_INVALID_ARGUMENT;
-  const int groups = norm_back_groups(rows, cols);
+  const int groups = norm_back_groups(rows, cols, true);
   *workspace_bytes = groups > 1 ? (size_t)groups * (size_t)cols * 4 : 0;
   return MUON_OK;
 }
@@ -279,7 +279,7 @@ muon_status muon_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, i
   p.ldh = ldh;
   p.lddh = lddh;
   p.lddx = lddx;
-  p.groups = norm_back_groups(rows, cols);
+  p.groups = norm_back_groups(rows, cols, dtype == MUON_BF16);
   p.part = p.groups > 1 ? (float*)workspace : dweight;
   hipError_t e = launch_norm_back(p, dtype == MUON_BF16, stream);
   if (e == hipSuccess && p.groups > 1) e = launch_norm_back_sum(p.part, dweight, p.groups, cols, stream);

@@ -6,8 +6,9 @@
 // written once.  A row belongs to 8 to 64 lanes of a wave up to 1024 columns (no
 // barrier), to 2, 4 or 16 waves above; each lane holds NC chunks of 8
 // consecutive columns (16 bytes of bf16).  Rows need no alignment: gfx950 takes 16-byte global
-// accesses at any address of the element's own alignment, and the ragged
-// last chunk of a row goes element by element.
+// accesses at any address of the element's own alignment (measured: 6.1 TB/s
+// off 16 bytes against 6.7 for a bare copy), and the ragged last chunk of a
+// row is read whole from where it fits and written element by element.
 //
 // The 8-bit form of a row v is scale = 2^e with the smallest e >= -126 for
 // which max|v| <= 127 * 2^e, and q = rint(v / scale).  A power of two makes
@@ -44,38 +45,77 @@ template <> struct Elem<I8> {
 // Eight consecutive elements as they lie in memory.
 template <typename T> struct Chunk { typename Elem<T>::type e[8]; };
 
-// Eight elements at p, of which n exist (none: n <= 0); the others are 0.
-// Non-temporal where a row is read once per step: it keeps the stream from
-// displacing what the next kernel reads.
+// The chunk at column c of a row of `cols`.  A chunk that the row's end cuts is
+// read whole from where it still fits, and one past the end as well (in
+// flight like any other; predicated element reads cost a latency each), and
+// mend8 puts it in place when it is used.  Rows under 8 columns go element by
+// element.  Non-temporal where a row is read once per step: it keeps the
+// stream from displacing what the next kernel reads.
 template <typename T, bool NT = false>
-__device__ __forceinline__ void fetch8(const typename Elem<T>::type* p, int n, Chunk<T>& c) {
+__device__ __forceinline__ void fetch8(const typename Elem<T>::type* row, int c, int cols, Chunk<T>& k) {
   typedef typename Elem<T>::type E;
-  if (n >= 8) {
+  if (cols >= 8) {
+    const E* p = row + min(c, cols - 8);
     if constexpr (NT && sizeof(E) > 1) {
       typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
       constexpr int NV = 8 * sizeof(E) / 16;
       V v[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] = __builtin_nontemporal_load((const V*)p + i);
-      __builtin_memcpy(c.e, v, sizeof(c.e));
+      __builtin_memcpy(k.e, v, sizeof(k.e));
     } else {
-      __builtin_memcpy(c.e, p, sizeof(c.e));
+      __builtin_memcpy(k.e, p, sizeof(k.e));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c.e[i] = i < n ? p[i] : (E)0;
+    for (int i = 0; i < 8; ++i) k.e[i] = c + i < cols ? row[c + i] : (E)0;
   }
 }
+// Elements c .. cols - 1 first, zeros behind them.
 template <typename T>
-__device__ __forceinline__ void widen8(const Chunk<T>& c, float v[8]) {
+__device__ __forceinline__ void mend8(Chunk<T>& k, int c, int cols) {
+  typedef typename Elem<T>::type E;
+  const int d = c + 8 - cols;  // elements that it was moved back by
+  if (d <= 0 || cols < 8) return;
+  if constexpr (sizeof(E) == 4) {
+    E e[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = Elem<T>::to(c.e[i]);
+    for (int i = 0; i < 8; ++i) e[i] = d & 4 ? (i < 4 ? k.e[i + 4] : 0.0f) : k.e[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = d & 2 ? (i < 6 ? e[i + 2] : 0.0f) : e[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = d & 1 ? (i < 7 ? e[i + 1] : 0.0f) : e[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k.e[i] = d >= 8 ? 0.0f : e[i];
+  } else if constexpr (sizeof(E) == 2) {
+    uint64_t w[2];
+    __builtin_memcpy(w, k.e, 16);
+    const int sh = (d & 3) * 16;
+    w[0] = d & 4 ? w[1] : w[0];
+    w[1] = d & 4 ? 0 : w[1];
+    w[0] = sh ? (w[0] >> sh) | (w[1] << (64 - sh)) : w[0];
+    w[1] >>= sh;
+    if (d >= 8) w[0] = w[1] = 0;
+    __builtin_memcpy(k.e, w, 16);
+  } else {
+    uint64_t w;
+    __builtin_memcpy(&w, k.e, 8);
+    w = d >= 8 ? 0 : w >> (d * 8);
+    __builtin_memcpy(k.e, &w, 8);
+  }
+}
+// (widens a chunk in place in its row)
+template <typename T>
+__device__ __forceinline__ void widen8(Chunk<T>& k, int c, int cols, float v[8]) {
+  mend8<T>(k, c, cols);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = Elem<T>::to(k.e[i]);
 }
 template <typename T>
-__device__ __forceinline__ void load8(const typename Elem<T>::type* p, int n, float v[8]) {
-  Chunk<T> c;
-  fetch8<T>(p, n, c);
-  widen8<T>(c, v);
+__device__ __forceinline__ void load8(const typename Elem<T>::type* row, int c, int cols, float v[8]) {
+  Chunk<T> k;
+  fetch8<T>(row, c, cols, k);
+  widen8<T>(k, c, cols, v);
 }
 
 template <bool NT = false, typename E>
@@ -162,33 +202,34 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p)
   // the widest rows (16 x 4 chunks, 128 registers per lane) read the weights
   // again from the caches where they are used
   constexpr bool KEEPW = LPR * NC < 4096;
-  float v[NC][8], wk[KEEPW ? NC : 1][8];
+  Chunk<F32> cw[KEEPW ? NC : 1];
+  float v[NC][8];
   auto weights = [&](int i, float w[8]) {
     if constexpr (KEEPW) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = wk[i][j];
+      for (int j = 0; j < 8; ++j) w[j] = cw[i].e[j];
     } else {
-      load8<F32>(p.w + c0 + i * STEP, cols - c0 - i * STEP, w);
+      load8<F32>(p.w, c0 + i * STEP, cols, w);
     }
   };
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = c0 + i * STEP;
-    fetch8<T, true>(x + c, cols - c, cx[i]);
-    if constexpr (RES) fetch8<T, true>(res + c, cols - c, cr[i]);
+    fetch8<T, true>(x, c, cols, cx[i]);
+    if constexpr (RES) fetch8<T, true>(res, c, cols, cr[i]);
   }
   if constexpr (MODE != 0 && KEEPW) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) load8<F32>(p.w + c0 + i * STEP, cols - c0 - i * STEP, wk[i]);
+    for (int i = 0; i < NC; ++i) fetch8<F32>(p.w, c0 + i * STEP, cols, cw[i]);
   }
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    widen8<T>(cx[i], v[i]);
+    const int c = c0 + i * STEP;
+    widen8<T>(cx[i], c, cols, v[i]);
     if constexpr (RES) {
-      const int c = c0 + i * STEP;
       float a[8];
       E e[8];
-      widen8<T>(cr[i], a);
+      widen8<T>(cr[i], c, cols, a);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         e[j] = Elem<T>::from(v[i][j] + a[j]);
@@ -196,6 +237,7 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p)
       }
       store8<true>((E*)p.h + row * p.ldh + c, cols - c, e);
     }
+    if constexpr (MODE != 0 && KEEPW) mend8<F32>(cw[i], c, cols);
   }
 
   double sum = 0.0;
@@ -293,13 +335,16 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p)
 //
 // Rows over 8192 columns (16 waves, 128 registers per lane): the running dw
 // lies in LDS, the weights come from the caches, nothing is fetched ahead, and
-// the row stays in its storage type, widened again for the second pass.
+// the row stays in its storage type, widened again for the second pass.  Over
+// 16384 columns it does not fit even so, and the second pass reads it again
+// (from L2: one row per compute unit, 3 MB per XCD).
 template <typename T, typename TH, int LPR, int NC>
 __global__ void __launch_bounds__(Rows<LPR>::NT) norm_back_kernel(const NormBackParams p) {
   typedef typename Elem<T>::type E;
   typedef typename Elem<TH>::type EH;
   typedef Rows<LPR> RW;
   constexpr bool WIDE = LPR * NC > 1024;
+  constexpr bool AGAIN = LPR * NC > 2048;
   constexpr int W = RW::JOIN ? RW::W : 1;
   __shared__ float s_dot[2][W];
   __shared__ float4 s_dw[WIDE || RW::RPB > 1 ? NC * 2 * RW::NT : 1];
@@ -316,24 +361,28 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_back_kernel(const NormBack
   } else {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      load8<F32>(p.w + c0 + i * STEP, cols - c0 - i * STEP, wk[i]);
+      load8<F32>(p.w, c0 + i * STEP, cols, wk[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) dwk[i][j] = 0.0f;
     }
   }
 
-  Chunk<T> cdy[NC], cdh[NC];
-  Chunk<TH> ch[NC];
-  auto fetch = [&](int64_t row) {
+  constexpr int KEPT = AGAIN ? 1 : NC;  // chunks of the row in registers
+  Chunk<T> cdy[KEPT], cdh[KEPT];
+  Chunk<TH> ch[KEPT];
+  auto fetch_one = [&](int64_t row, int i) {
     const E* dyr = (const E*)p.dy + row * p.lddy;
     const EH* hr = (const EH*)p.h + row * p.ldh;
     const E* dhr = (const E*)p.dh + row * p.lddh;
+    const int c = c0 + i * STEP, k = AGAIN ? 0 : i;
+    fetch8<T, !AGAIN>(dyr, c, cols, cdy[k]);
+    fetch8<TH, !AGAIN>(hr, c, cols, ch[k]);
+    if (p.dh) fetch8<T, !AGAIN>(dhr, c, cols, cdh[k]);
+  };
+  auto fetch = [&](int64_t row) {
+    if constexpr (!AGAIN) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int c = c0 + i * STEP;
-      fetch8<T, true>(dyr + c, cols - c, cdy[i]);
-      fetch8<TH, true>(hr + c, cols - c, ch[i]);
-      if (p.dh) fetch8<T, true>(dhr + c, cols - c, cdh[i]);
+      for (int i = 0; i < NC; ++i) fetch_one(row, i);
     }
   };
   const int64_t first = (int64_t)blockIdx.x * RW::RPB + threadIdx.x / LPR, stride = (int64_t)p.groups * RW::RPB;
@@ -346,8 +395,10 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_back_kernel(const NormBack
     if constexpr (sizeof(EH) == 1) hs = p.hscale[row];
     // g and hat of chunk i
     auto terms = [&](int i, const float w[8], float dy[8], float g[8], float hat[8]) {
-      widen8<T>(cdy[i], dy);
-      widen8<TH>(ch[i], hat);
+      Chunk<T> k = cdy[AGAIN ? 0 : i];  // (copies: the wide rows widen theirs twice)
+      Chunk<TH> kh = ch[AGAIN ? 0 : i];
+      widen8<T>(k, c0 + i * STEP, cols, dy);
+      widen8<TH>(kh, c0 + i * STEP, cols, hat);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         hat[j] *= hs;
@@ -358,14 +409,15 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_back_kernel(const NormBack
     float g[WIDE ? 1 : NC][8], hat[WIDE ? 1 : NC][8];
     Chunk<T> cadd[WIDE ? 1 : NC];
     float dot = 0.0f;
-#pragma unroll
+#pragma unroll AGAIN ? 1 : NC
     for (int i = 0; i < NC; ++i) {
+      if constexpr (AGAIN) fetch_one(row, i);
       float dy[8];
       float *gi = g[WIDE ? 0 : i], *hi = hat[WIDE ? 0 : i];
       if constexpr (WIDE) {
         float w[8], dw[8];
         float4* l = s_dw + 2 * i * LPR + threadIdx.x;
-        load8<F32>(p.w + c0 + i * STEP, cols - c0 - i * STEP, w);
+        load8<F32>(p.w, c0 + i * STEP, cols, w);
         terms(i, w, dy, gi, hi);
         __builtin_memcpy(dw, l, 16);
         __builtin_memcpy(dw + 4, l + LPR, 16);
@@ -393,20 +445,21 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_back_kernel(const NormBack
     }
     dot *= inv_cols;
     E* dxr = (E*)p.dx + row * p.lddx;
-#pragma unroll
+#pragma unroll AGAIN ? 1 : NC
     for (int i = 0; i < NC; ++i) {
       const int c = c0 + i * STEP;
       if (c < cols) {
+        if constexpr (AGAIN) fetch_one(row, i);
         E e[8];
         float dh[8];
         float *gi = g[WIDE ? 0 : i], *hi = hat[WIDE ? 0 : i];
         if constexpr (WIDE) {
           float w[8], dy[8];
-          load8<F32>(p.w + c, cols - c, w);
+          load8<F32>(p.w, c, cols, w);
           terms(i, w, dy, gi, hi);
         }
         if (p.dh) {
-          widen8<T>(WIDE ? cdh[i] : cadd[WIDE ? 0 : i], dh);
+          widen8<T>(WIDE ? cdh[AGAIN ? 0 : i] : cadd[WIDE ? 0 : i], c, cols, dh);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) dh[j] = 0.0f;
@@ -475,24 +528,35 @@ __global__ void __launch_bounds__(1024) norm_back_sum_kernel(const float* part, 
   if (g0 == 0 && c < cols) dw[c] = s[0][cl];
 }
 
-// x = q * scale.  The matrix is cut into chunks of 8 columns, one per thread.
+// x = q * scale.  The matrix is cut into chunks of 16 stored bytes (8 bf16 or 4
+// fp32 columns), one per thread.
 template <typename T>
 __global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* q, int64_t ldq, const float* scale,
                                                          typename Elem<T>::type* x, int64_t ldx, int64_t rows,
                                                          int cols) {
   typedef typename Elem<T>::type E;
-  const uint32_t cpr = (uint32_t)(cols + 7) / 8;
+  constexpr int C = 16 / sizeof(E);
+  const uint32_t cpr = (uint32_t)(cols + C - 1) / C;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = id >> 32 ? id / cpr : (int64_t)((uint32_t)id / cpr);
   if (row >= rows) return;
-  const int col = (int)(id - row * cpr) * 8, n = cols - col;
-  float v[8];
-  E e[8];
-  load8<I8>(q + row * ldq + col, n, v);
+  const int col = (int)(id - row * cpr) * C, n = cols - col;
+  const int8_t* a = q + row * ldq + col;
+  E* o = x + row * ldx + col;
   const float s = scale[row];
+  if (n >= C) {
+    int8_t v[C];
+    E e[C];
+    __builtin_memcpy(v, a, C);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) e[j] = Elem<T>::from(v[j] * s);
-  store8<true>(x + row * ldx + col, n, e);
+    for (int j = 0; j < C; ++j) e[j] = Elem<T>::from((float)v[j] * s);
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
+    V w;
+    __builtin_memcpy(&w, e, 16);
+    __builtin_nontemporal_store(w, (V*)o);
+  } else {
+    for (int j = 0; j < n; ++j) o[j] = Elem<T>::from((float)a[j] * s);
+  }
 }
 
 template <typename T, int MODE, bool RES, int LPR, int NC>
@@ -542,9 +606,9 @@ hipError_t pick_back(const NormBackParams& p, hipStream_t s) {
   if (d <= 256) return go_back<T, TH, 16, 2>(p, s);
   if (d <= 512) return go_back<T, TH, 32, 2>(p, s);
   if (d <= 1024) return go_back<T, TH, 64, 2>(p, s);
-  if (d <= 2048) return go_back<T, TH, 64, 4>(p, s);
+  if (d <= 2048) return go_back<T, TH, 256, 1>(p, s);
   if (d <= 4096) return go_back<T, TH, 256, 2>(p, s);
-  if (d <= 8192) return go_back<T, TH, 512, 2>(p, s);
+  if (d <= 8192) return go_back<T, TH, 1024, 1>(p, s);
   if (d <= 16384) return go_back<T, TH, 1024, 2>(p, s);
   return go_back<T, TH, 1024, 4>(p, s);
 }
@@ -557,13 +621,16 @@ hipError_t launch_norm(const NormParams& p, bool bf16, hipStream_t s) {
 
 // Workgroups of the backward pass: enough to fill the chip, few enough that
 // the partial dw rows stay small beside the rows themselves.  Measured over
-// 29.4 M bf16 elements with dh (us, sums included) for 256 / 512 / 1024
-// groups: 53 / 45 / 50 at 1024 columns, 61 / 49 / 58 at 3584, 51 / 56 / 67 at
-// 8192.
-int norm_back_groups(int64_t rows, int64_t cols) {
-  const int64_t side = cols <= 128 ? 32 : cols <= 256 ? 16 : cols <= 512 ? 8 : cols <= 2048 ? 4 : 1;  // RPB
-  const int64_t full = cols <= 4096 ? 512 : 256;
+// 29.4 M bf16 elements (us, sums included) for 256 / 512 / 768 / 1024 groups,
+// with dh: 59 / 48 / 47 / 53 at 1024 columns, 64 / 50 / 50 / 60 at 3584, 49 /
+// 54 / 60 / 66 at 8192; from 8-bit rows without dh: 52 / 37 / 33 / 41, 59 / 41
+// / 37 / 48 and 40 / 45 / 51 / 56.  Fp32 rows (twice the bytes in flight) and
+// short batches do better with 512 (f32, 8192 x 3584, dh: 90 against 107; bf16,
+// 2048 x 4096: 21 against 24).
+int norm_back_groups(int64_t rows, int64_t cols, bool bf16) {
+  const int64_t side = cols <= 128 ? 32 : cols <= 256 ? 16 : cols <= 512 ? 8 : cols <= 1024 ? 4 : 1;  // RPB
   const int64_t need = (rows + side - 1) / side;
+  const int64_t full = cols > 4096 ? 256 : bf16 && need >= 4096 ? 768 : 512;
   return (int)(need < full ? need : full);
 }
 
@@ -593,7 +660,7 @@ hipError_t launch_quantize(const void* x, int64_t ldx, int8_t* q, int64_t ldq, f
 
 hipError_t launch_dequantize(const int8_t* q, int64_t ldq, const float* scale, void* x, int64_t ldx,
                              int64_t rows, int64_t cols, bool bf16, hipStream_t s) {
-  const int64_t blocks = (rows * ((cols + 7) / 8) + 255) / 256;
+  const int64_t per = bf16 ? 8 : 4, blocks = (rows * ((cols + per - 1) / per) + 255) / 256;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)blocks);
   if (bf16)
