@@ -298,7 +298,10 @@ struct Reader {
   }
 };
 
-// Four consecutive outputs of one row, n of which exist.
+// Four consecutive outputs of one row, n of which exist.  STREAM: past the
+// caches, for stores that fill whole lines (partial ones have to meet in L2:
+// streamed, an output of 18944 x 3584 took 94 us instead of 60).
+template <bool STREAM = false>
 __device__ __forceinline__ void put4(const MmParams& p, int64_t at, int n, const float v[4]) {
   if (p.obf16) {
     uint16_t* o = (uint16_t*)p.out + at;
@@ -316,17 +319,34 @@ __device__ __forceinline__ void put4(const MmParams& p, int64_t at, int n, const
   } else {
     float* o = (float*)p.out + at;
     if (n >= 4) {
-      float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (p.accumulate) __builtin_memcpy(e, o, 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = p.accumulate ? e[i] + v[i] : v[i];
-      __builtin_memcpy(o, e, 16);
+      typedef float V __attribute__((ext_vector_type(4), aligned(4)));
+      V e = {v[0], v[1], v[2], v[3]};
+      if (p.accumulate) e += *(const V*)o;
+      if constexpr (STREAM) __builtin_nontemporal_store(e, (V*)o);
+      else *(V*)o = e;
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (i < n) o[i] = p.accumulate ? o[i] + v[i] : v[i];
     }
   }
+}
+// Eight of a bf16 row.
+__device__ __forceinline__ void put8(const MmParams& p, int64_t at, int n, const float v[8]) {
+  if (n < 8) {
+    put4(p, at, n, v);
+    if (n > 4) put4(p, at + 4, n - 4, v + 4);
+    return;
+  }
+  typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
+  uint16_t* o = (uint16_t*)p.out + at;
+  uint16_t e[8];
+  if (p.accumulate) __builtin_memcpy(e, o, 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = to_bf16(p.accumulate ? bf16_bits_to_f32(e[i]) + v[i] : v[i]);
+  V w;
+  __builtin_memcpy(&w, e, 16);
+  __builtin_nontemporal_store(w, (V*)o);
 }
 
 template <bool C> struct Cut { static constexpr bool value = C; };
@@ -592,36 +612,89 @@ __global__ void __launch_bounds__(64 * waves_of(T) * G, T == 128 && G == 1 ? 2 :
       }
   }
 
-  // acc[i][j][e] is column col0 + 16 i + 4 q4 + e of row row0 + 16 j + c16
-  const int colt = wp * (T / 2) + 4 * q4, rowt = wq * (T / WQ) + c16;
-  if (splits > 1) {  // the raw sums, tile by tile
-    float* part = p.part + ((int64_t)(tile - p.direct) * splits + split) * (T * T);
-#pragma unroll
-    for (int j = 0; j < FQ; ++j)
-#pragma unroll
-      for (int i = 0; i < FP; ++i)
-        if (G == 1 || (i * FQ + j) % G == group) *(Acc*)(part + (rowt + 16 * j) * T + colt + 16 * i) = acc[i][j];
-    return;
-  }
+  // acc[i][j][e] is column 16 i + 4 q4 + e of row 16 j + c16 of the wave's part
+  const int colt = wp * (T / 2), rowt = wq * (T / WQ);
   const int col0 = tp * T + colt, row0 = tq * T + rowt;
+  float* const part = p.part + ((int64_t)(tile - p.direct) * splits + split) * (T * T);
+  if constexpr (T > 64) {
+    // A lane's four columns are 16 bytes of a row 16 rows apart from its
+    // neighbours'.  Sixteen rows of the wave's part at a time go through LDS,
+    // 16-byte chunks swapped within a row by the row's number (no bank
+    // conflicts either way), and leave as whole rows: 256 bytes or more each.
+    constexpr int PT = 16 * FP, CPR = PT / 4;  // columns and chunks of a row
+    static_assert(NW * 16 * PT * 4 * G <= G * D * OPB, "the staged rows fit a ring");
+    if constexpr (G == 1) barrier();  // no wave reads the rings any more
+    char* const st = s_q + (group * NW + wave) * (16 * PT * 4);
+    auto chunk = [&](int r, int c) { return st + r * (PT * 4) + ((c ^ (r & (CPR - 1))) << 4); };
 #pragma unroll
-  for (int j = 0; j < FQ; ++j) {
-    const int r = row0 + 16 * j;
-    if (r >= p.nq) continue;
-    float sq = 1.0f;
-    if (I8K) sq = p.sq[r];
+    for (int j = 0; j < FQ; ++j) {
+      if (G > 1 && j % G != group) continue;  // (FQ is a multiple of G: block (i, j) is group j % G's)
+      const int r = row0 + 16 * j + c16;
+      float sq = 1.0f;
+      if (I8K && splits == 1) sq = p.sq[min(r, p.nq - 1)];
 #pragma unroll
-    for (int i = 0; i < FP; ++i) {
-      const int c = col0 + 16 * i;
-      const int n = p.np - c;
-      if (n <= 0 || (G > 1 && (i * FQ + j) % G != group)) continue;
-      float v[4];
+      for (int i = 0; i < FP; ++i) {
+        f32x4 v;
+        if (splits > 1) {
+          v = __builtin_bit_cast(f32x4, acc[i][j]);
+        } else {
+          const int c = col0 + 16 * i + 4 * q4;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = (float)acc[i][j][e];
-        if constexpr (I8K) v[e] = v[e] * sq * p.sp[min(c + e, p.np - 1)];
+          for (int e = 0; e < 4; ++e) {
+            v[e] = (float)acc[i][j][e];
+            if constexpr (I8K) v[e] = v[e] * sq * p.sp[min(c + e, p.np - 1)];
+          }
+        }
+        *(f32x4*)chunk(c16, 4 * i + q4) = v;
       }
-      put4(p, (int64_t)r * p.ldo + c, n, v);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (splits > 1 || !p.obf16) {
+#pragma unroll
+        for (int it = 0; it < CPR / 4; ++it) {
+          const int at = it * 64 + lane, rr = at / CPR, ch = at % CPR;
+          const f32x4 v = *(const f32x4*)chunk(rr, ch);
+          if (splits > 1) {
+            *(f32x4*)(part + (rowt + 16 * j + rr) * T + colt + 4 * ch) = v;
+          } else {
+            const int ro = row0 + 16 * j + rr, c = col0 + 4 * ch, n = p.np - c;
+            const float o[4] = {v[0], v[1], v[2], v[3]};
+            if (ro < p.nq && n > 0) put4<true>(p, (int64_t)ro * p.ldo + c, n, o);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int it = 0; it < CPR / 8; ++it) {
+          const int at = it * 64 + lane, rr = at / (CPR / 2), ch = at % (CPR / 2) * 2;
+          const f32x4 v = *(const f32x4*)chunk(rr, ch), w = *(const f32x4*)chunk(rr, ch + 1);
+          const int ro = row0 + 16 * j + rr, c = col0 + 4 * ch, n = p.np - c;
+          const float o[8] = {v[0], v[1], v[2], v[3], w[0], w[1], w[2], w[3]};
+          if (ro < p.nq && n > 0) put8(p, (int64_t)ro * p.ldo + c, n, o);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+      const int r = 16 * j + c16;
+#pragma unroll
+      for (int i = 0; i < FP; ++i) {
+        if ((i * FQ + j) % G != group) continue;
+        const int c = 16 * i + 4 * q4, n = p.np - col0 - c;
+        if (splits > 1) {  // the raw sums
+          *(Acc*)(part + (rowt + r) * T + colt + c) = acc[i][j];
+        } else if (row0 + r < p.nq && n > 0) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = (float)acc[i][j][e];
+            if constexpr (I8K) v[e] = v[e] * p.sq[row0 + r] * p.sp[min(col0 + c + e, p.np - 1)];
+          }
+          put4(p, (int64_t)(row0 + r) * p.ldo + col0 + c, n, v);
+        }
+      }
     }
   }
 }
