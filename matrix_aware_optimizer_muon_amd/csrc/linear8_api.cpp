@@ -68,20 +68,55 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
   const bool off_p = i8 && (!aligned(b, 16) || c.ldp % 16 || b_cols % 16);
   auto tiles = [&](int64_t T) { return (int64_t)((c.np + T - 1) / T) * ((c.nq + T - 1) / T); };
   const int64_t stages = (c.kd + (i8 ? 63 : 31)) / (i8 ? 64 : 32);
-  // Tiles by how many there are of them: 256-wide from three quarters of the
-  // compute units on; below, the smallest with at most one per unit, whose
-  // wave groups share K (groups), else 128-wide.  Measured (us, integer
-  // product of 300 x 2880 from 1408: 64-wide 6.6, 128 11.5; input gradient of
-  // 1024 x 3584 from 3584: 128 with two groups 39, one group 50, 256-wide 48).
+  // A way to run it, and its time without what every way has.  Workgroups that
+  // run at once (slots: one per compute unit, two of 128-wide tiles with one
+  // group) take a tile each in whole rounds; the tiles left over may be split
+  // along K over one more round.  Measured: a stage takes 0.3 us in 64-wide
+  // integer tiles, 0.55 in the gradients', 0.6 in 128-wide ones, 1 in 256-wide
+  // ones; a split costs a second launch (4 us) and its partial sums' way to
+  // memory and back (at 4 TB/s).  So a weight gradient of 512 x 3584 from 4096
+  // tokens is split (31 against 43 us), a product of 4096 x 512 from 3584 is
+  // not (16 against 24).
+  struct Way {
+    int tile, groups, splits, direct;
+    double us;
+  };
+  auto way = [&](int tile, int groups) {
+    const int64_t all = tiles(tile), slots = tile == 128 && groups == 1 ? 512 : 256, rest = all % slots;
+    const int64_t each = (stages + groups - 1) / groups;  // a group's stages
+    const double stage_us = tile == 256 ? 1.0 : tile == 128 ? 0.6 : i8 ? 0.3 : 0.55;
+    Way w = {tile, groups, 1, (int)all, stage_us * (double)each};
+    const double tile_us = (double)tile * tile * 8 / 4e6;  // written and read
+    const int64_t most = rest > 0 ? std::min<int64_t>({slots / rest, each / 4, 32}) : 1;
+    for (int64_t n = 2; n <= most; ++n) {
+      const double us = stage_us * (double)((each + n - 1) / n) + 4.0 + tile_us * (double)(rest * n);
+      if (us < w.us) {
+        w.us = us;
+        w.splits = (int)n;
+        w.direct = (int)(all - rest);
+      }
+    }
+    return w;
+  };
+  // 256-wide tiles from three quarters of the compute units on.  Below, 64- or
+  // 128-wide ones that are at most one per unit, with wave groups sharing K,
+  // whichever is faster by the above (integer product of 300 x 2880 from 1408:
+  // 64-wide 6.6 us, 128-wide 11.5; input gradient of 128 x 3584 from 18944:
+  // 60 and 36); else 128-wide ones with one group.
+  Way w;
   if (tiles(256) >= 192) {
-    c.tile = 256;
-  } else if (tiles(64) <= 256) {
-    c.tile = 64;
-    c.groups = 4;
+    w = way(256, 1);
   } else {
-    c.tile = 128;
-    c.groups = tiles(128) <= 256 ? 2 : 1;
+    w = way(128, tiles(128) <= 256 ? 2 : 1);
+    if (tiles(64) <= 256) {
+      const Way small = way(64, 4);
+      if (small.us < w.us) w = small;
+    }
   }
+  c.tile = w.tile;
+  c.groups = w.groups;
+  c.splits = w.splits;
+  c.direct = w.direct;
   if (c.tile == 256) {
     c.pack_q = off_q;
     c.pack_p = off_p;
@@ -104,29 +139,9 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
     c.at_p = c.bytes;
     c.bytes += up(b_rows * c.ldp, 256);
   }
-  // Workgroups that run at once: whole rounds of them take a tile each; the
-  // tiles left over may be split along K over one more round.  A split costs a
-  // second launch (4 us) and its partial sums' way to memory and back (at 4
-  // TB/s), and saves a part of the stages: 0.3 us each for the integer
-  // product's small tiles, 0.55 us for the gradients', 1 us for 256-wide ones
-  // (measured).  So a weight gradient of 512 x 3584 from 4096 tokens is split
-  // (33 against 43 us), a product of 4096 x 512 from 3584 is not (18 against
-  // 26).  128-wide tiles of one group run two to a compute unit.
-  const int64_t all = tiles(c.tile);
-  const int64_t slots = c.tile == 128 && c.groups == 1 ? 512 : 256, rest = all % slots;
-  const int64_t each = stages / c.groups;  // a group's stages
-  c.direct = (int)all;
-  if (rest > 0) {
-    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({slots / rest, each / 4, 32}));
-    const double tile_us = (double)c.tile * c.tile * 8 / 4e6;  // written and read
-    const double stage_us = c.tile == 256 ? 1.0 : i8 ? 0.3 : 0.55;
-    const double saved = stage_us * (double)(each - each / c.splits), cost = 4.0 + tile_us * (double)(rest * c.splits);
-    if (saved < cost) c.splits = 1;
-    if (c.splits > 1) {
-      c.direct = (int)(all - rest);
-      c.at_part = c.bytes;
-      c.bytes += rest * c.splits * c.tile * c.tile * 4;
-    }
+  if (c.splits > 1) {
+    c.at_part = c.bytes;
+    c.bytes += (tiles(c.tile) - c.direct) * c.splits * c.tile * c.tile * 4;
   }
   return c;
 }
