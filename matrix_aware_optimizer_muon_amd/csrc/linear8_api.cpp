@@ -169,7 +169,8 @@ muon_status run_product(muon_q8_product kind, const void* a, int64_t lda, const 
   if (!matrix(out, ldo, o_rows, o_cols, size_of(dtype))) return MUON_ERR_INVALID_ARGUMENT;
   if (t * a_cols > 0 && !matrix(a, lda, t, a_cols, i8 ? 1 : 2)) return MUON_ERR_INVALID_ARGUMENT;
   if (b_rows * k > 0 && !matrix(b, ldb, b_rows, k, 1)) return MUON_ERR_INVALID_ARGUMENT;
-  if ((i8 && !a_scale) || (b_rows > 0 && !b_scale)) return MUON_ERR_INVALID_ARGUMENT;
+  if ((i8 && !a_scale) || (b_rows > 0 && !b_scale) || !aligned(a_scale, 4) || !aligned(b_scale, 4))
+    return MUON_ERR_INVALID_ARGUMENT;
   const Choice c = choose(kind, a, lda, b, ldb, t, n, k);
   if (c.bytes > 0) {
     if (workspace_bytes < (size_t)c.bytes) return MUON_ERR_WORKSPACE_TOO_SMALL;

@@ -11,7 +11,8 @@ gradient that a Muon step takes, with activations and weights kept in 8 bits.
 An 8-bit tensor is a `Q8`: int8 rows and one power-of-two fp32 scale per row
 (value = q * scale).  Tensors are CUDA tensors with unit stride in the last
 dimension; 2-D ones may have any row stride, others are taken as rows of their
-last dimension and must be contiguous.  Work is enqueued on the current
+last dimension and must be contiguous.  Forward and backward are calls of
+their own: nothing is recorded for autograd.  Work is enqueued on the current
 stream of the tensors' device; results and workspaces come from torch's
 allocator.  Argument errors raise ValueError, or MuonError from the C ABI.
 

@@ -415,6 +415,28 @@ def test_gradient_products_keep_non_finite_values_in_their_place(t, n, k):
     assert torch.equal(di[:t - 1], ci[:t - 1]) and torch.equal(dw[:n - 1], cw[:n - 1])
 
 
+def test_gradient_products_against_differences():
+    t, n, k = 9, 40, 33
+    x, w, c = q8rand(t, k, 1), q8rand(n, k, 2), rand((t, n), 3, BF)
+    di, dw = l8.grad_input(c, w, F32), l8.grad_weight(c, x, F32)
+    xd, wd, cd = dense(x), dense(w), c.double()
+
+    def loss(xv, wv):
+        return float((xv @ wv.t().contiguous() * cd).sum())
+
+    # the loss is linear in each operand: a difference of any width is exact but
+    # for the 64-bit sums
+    for i, j, m in ((0, 0, 0), (4, 17, 20), (8, 39, 32)):
+        d = torch.zeros_like(xd)
+        d[i, m] = 1.0
+        num = (loss(xd + d, wd) - loss(xd - d, wd)) / 2
+        assert abs(num - float(di[i, m])) <= (n + 40) * 2 * U * float(cd[i].abs() @ wd[:, m].abs()) + 1e-9
+        d = torch.zeros_like(wd)
+        d[j, m] = 1.0
+        num = (loss(xd, wd + d) - loss(xd, wd - d)) / 2
+        assert abs(num - float(dw[j, m])) <= (t + 40) * 2 * U * float(cd[:, j].abs() @ xd[:, m].abs()) + 1e-9
+
+
 def run_all(x, r, w, wq, dout):
     y, h, rstd = l8.rmsnorm(x, w, residual=r, q8=True)
     out = l8.matmul(y, wq)

@@ -94,7 +94,7 @@ def product(kind, t=40, n=48, k=64, a=P, lda=None, s=P, b=P, ldb=None, out=P, ld
 @pytest.mark.parametrize("kw, want", [
     ({"t": -1}, INVALID), ({"n": -1}, INVALID), ({"k": -1}, INVALID), ({"t": (1 << 24) + 1}, UNSUPPORTED),
     ({"dtype": 2}, INVALID), ({"a": 0}, INVALID), ({"b": 0}, INVALID), ({"out": 0}, INVALID),
-    ({"out": P + 2}, INVALID), ({"s": 0}, INVALID), ({"lda": 20}, INVALID), ({"ldb": 20}, INVALID),
+    ({"out": P + 2}, INVALID), ({"s": 0}, INVALID), ({"s": P + 2}, INVALID), ({"lda": 20}, INVALID), ({"ldb": 20}, INVALID),
     ({"ldo": 20}, INVALID)])
 def test_product_refusals(kind, kw, want):
     assert product(kind, **kw) == want
