@@ -430,6 +430,28 @@ __global__ void __launch_bounds__(64 * waves_of(T) * G, T == 128 && G == 1 ? 2 :
 #pragma unroll
     for (int j = 0; j < FQ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
+  // acc[i][j][e] is column 16 i + 4 q4 + e of row 16 j + c16 of the wave's part
+  const int colt = wp * (T / 2), rowt = wq * (T / WQ);
+  const int col0 = tp * T + colt, row0 = tq * T + rowt;
+  // Tiles over 64 leave through LDS in whole rows: a lane's columns there, 8
+  // of a bf16 row (`wide`), else 4.  The smaller ones: a lane's own block.
+  const bool wide = splits == 1 && p.obf16;
+  const int outc = T > 64 ? (wide ? lane % (T / 16) * 8 : lane % (T / 8) * 4) : 16 * (group / FQ) + 4 * q4;
+  // (the integer product's scales are here before they are due: read at the
+  // end, they cost each tile a trip to memory)
+  float sq[T > 64 ? FQ : 1];
+  f32x4 sp[2];
+  if constexpr (I8K) {
+    if (splits == 1) {
+#pragma unroll
+      for (int j = 0; j < (T > 64 ? FQ : 1); ++j)
+        sq[j] = p.sq[min(row0 + 16 * (T > 64 ? j : group % FQ) + c16, p.nq - 1)];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < 4 || T > 64) sp[e / 4][e % 4] = p.sp[min(col0 + outc + e, p.np - 1)];
+    }
+  }
+
   if (steps > 0) {  // (an empty sum reads nothing)
     DmaP dp;
     DmaQ dq;
@@ -612,89 +634,85 @@ __global__ void __launch_bounds__(64 * waves_of(T) * G, T == 128 && G == 1 ? 2 :
       }
   }
 
-  // acc[i][j][e] is column 16 i + 4 q4 + e of row 16 j + c16 of the wave's part
-  const int colt = wp * (T / 2), rowt = wq * (T / WQ);
-  const int col0 = tp * T + colt, row0 = tq * T + rowt;
   float* const part = p.part + ((int64_t)(tile - p.direct) * splits + split) * (T * T);
   if constexpr (T > 64) {
     // A lane's four columns are 16 bytes of a row 16 rows apart from its
     // neighbours'.  Sixteen rows of the wave's part at a time go through LDS,
     // 16-byte chunks swapped within a row by the row's number (no bank
     // conflicts either way), and leave as whole rows: 256 bytes or more each.
+    // One loop over the blocks of rows, not unrolled but for its first lines:
+    // the code is fetched anew by each launch.
     constexpr int PT = 16 * FP, CPR = PT / 4;  // columns and chunks of a row
     static_assert(NW * 16 * PT * 4 * G <= G * D * OPB, "the staged rows fit a ring");
     if constexpr (G == 1) barrier();  // no wave reads the rings any more
     char* const st = s_q + (group * NW + wave) * (16 * PT * 4);
     auto chunk = [&](int r, int c) { return st + r * (PT * 4) + ((c ^ (r & (CPR - 1))) << 4); };
+    const int ch = outc / 4, n = p.np - (col0 + outc);
+#pragma clang loop unroll(disable)
+    for (int jr = G > 1 ? group : 0; jr < FQ; jr += G) {  // (FQ is a multiple of G: block (i, j) is group j % G's)
 #pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      if (G > 1 && j % G != group) continue;  // (FQ is a multiple of G: block (i, j) is group j % G's)
-      const int r = row0 + 16 * j + c16;
-      float sq = 1.0f;
-      if (I8K && splits == 1) sq = p.sq[min(r, p.nq - 1)];
+      for (int j = 0; j < FQ; ++j)
+        if (j == jr) {
 #pragma unroll
-      for (int i = 0; i < FP; ++i) {
-        f32x4 v;
-        if (splits > 1) {
-          v = __builtin_bit_cast(f32x4, acc[i][j]);
-        } else {
-          const int c = col0 + 16 * i + 4 * q4;
+          for (int i = 0; i < FP; ++i) {
+            f32x4 v;
+            if (I8K && splits == 1) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = (float)acc[i][j][e];
-            if constexpr (I8K) v[e] = v[e] * sq * p.sp[min(c + e, p.np - 1)];
+              for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][e] * sq[j];
+            } else {
+              v = __builtin_bit_cast(f32x4, acc[i][j]);
+            }
+            *(f32x4*)chunk(c16, 4 * i + q4) = v;
           }
         }
-        *(f32x4*)chunk(c16, 4 * i + q4) = v;
-      }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      if (splits > 1 || !p.obf16) {
-#pragma unroll
-        for (int it = 0; it < CPR / 4; ++it) {
-          const int at = it * 64 + lane, rr = at / CPR, ch = at % CPR;
-          const f32x4 v = *(const f32x4*)chunk(rr, ch);
+      const int r0 = row0 + 16 * jr;
+      if (!wide) {
+        constexpr int RPI = 64 / CPR;  // rows per instruction
+        int rr = lane / CPR;
+#pragma unroll 4
+        for (int it = 0; it < 16 / RPI; ++it, rr += RPI) {
+          f32x4 v = *(const f32x4*)chunk(rr, ch);
           if (splits > 1) {
-            *(f32x4*)(part + (rowt + 16 * j + rr) * T + colt + 4 * ch) = v;
-          } else {
-            const int ro = row0 + 16 * j + rr, c = col0 + 4 * ch, n = p.np - c;
+            *(f32x4*)(part + (rowt + 16 * jr + rr) * T + colt + outc) = v;
+          } else if (r0 + rr < p.nq && n > 0) {
+            if constexpr (I8K) v *= sp[0];
             const float o[4] = {v[0], v[1], v[2], v[3]};
-            if (ro < p.nq && n > 0) put4<true>(p, (int64_t)ro * p.ldo + c, n, o);
+            put4<true>(p, (int64_t)(r0 + rr) * p.ldo + col0 + outc, n, o);
           }
         }
       } else {
-#pragma unroll
-        for (int it = 0; it < CPR / 8; ++it) {
-          const int at = it * 64 + lane, rr = at / (CPR / 2), ch = at % (CPR / 2) * 2;
-          const f32x4 v = *(const f32x4*)chunk(rr, ch), w = *(const f32x4*)chunk(rr, ch + 1);
-          const int ro = row0 + 16 * j + rr, c = col0 + 4 * ch, n = p.np - c;
+        constexpr int RPI = 128 / CPR;
+        int rr = lane / (CPR / 2);
+#pragma unroll 2
+        for (int it = 0; it < 16 / RPI; ++it, rr += RPI) {
+          f32x4 v = *(const f32x4*)chunk(rr, ch), w = *(const f32x4*)chunk(rr, ch + 1);
+          if constexpr (I8K) v *= sp[0], w *= sp[1];
           const float o[8] = {v[0], v[1], v[2], v[3], w[0], w[1], w[2], w[3]};
-          if (ro < p.nq && n > 0) put8(p, (int64_t)ro * p.ldo + c, n, o);
+          if (r0 + rr < p.nq && n > 0) put8(p, (int64_t)(r0 + rr) * p.ldo + col0 + outc, n, o);
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
     }
   } else {
+    static_assert(FP * FQ == G, "one block per group");
+    const int r = 16 * (group % FQ) + c16, n = p.np - col0 - outc;
+    Acc a = acc[0][0];
 #pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      const int r = 16 * j + c16;
+    for (int b = 1; b < FP * FQ; ++b)
+      if (b == group) a = acc[b / FQ][b % FQ];
+    if (splits > 1) {  // the raw sums
+      *(Acc*)(part + (rowt + r) * T + colt + outc) = a;
+    } else if (row0 + r < p.nq && n > 0) {
+      float v[4];
 #pragma unroll
-      for (int i = 0; i < FP; ++i) {
-        if ((i * FQ + j) % G != group) continue;
-        const int c = 16 * i + 4 * q4, n = p.np - col0 - c;
-        if (splits > 1) {  // the raw sums
-          *(Acc*)(part + (rowt + r) * T + colt + c) = acc[i][j];
-        } else if (row0 + r < p.nq && n > 0) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = (float)acc[i][j][e];
-            if constexpr (I8K) v[e] = v[e] * p.sq[row0 + r] * p.sp[min(col0 + c + e, p.np - 1)];
-          }
-          put4(p, (int64_t)(row0 + r) * p.ldo + col0 + c, n, v);
-        }
+      for (int e = 0; e < 4; ++e) {
+        v[e] = (float)a[e];
+        if constexpr (I8K) v[e] = v[e] * sq[0] * sp[0][e];
       }
+      put4(p, (int64_t)(row0 + r) * p.ldo + col0 + outc, n, v);
     }
   }
 }
