@@ -68,15 +68,16 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
   const bool off_p = i8 && (!aligned(b, 16) || c.ldp % 16 || b_cols % 16);
   auto tiles = [&](int64_t T) { return (int64_t)((c.np + T - 1) / T) * ((c.nq + T - 1) / T); };
   const int64_t stages = (c.kd + (i8 ? 63 : 31)) / (i8 ? 64 : 32);
-  // A way to run it, and its time without what every way has.  Workgroups that
-  // run at once (slots: one per compute unit, two of 128-wide tiles with one
-  // group) take a tile each in whole rounds; the tiles left over may be split
-  // along K over one more round.  Measured: a stage takes 0.3 us in 64-wide
-  // integer tiles, 0.55 in the gradients', 0.6 in 128-wide ones, 1 in 256-wide
-  // ones; a split costs a second launch (4 us) and its partial sums' way to
-  // memory and back (at 4 TB/s).  So a weight gradient of 512 x 3584 from 4096
-  // tokens is split (31 against 43 us), a product of 4096 x 512 from 3584 is
-  // not (16 against 24).
+  // A way to run it, and its time.  Workgroups that run at once (slots: one
+  // per compute unit, two of 128-wide tiles with one group) take a tile each in
+  // whole rounds; the tiles left over may be split along K over one more round.
+  // Measured: a stage takes 0.3 us in 64-wide integer tiles (0.5 unaligned),
+  // 0.55 in the gradients', 0.55 (0.8) and 0.6 in 128-wide ones, 0.75 and 0.85
+  // in 256-wide ones; what is ahead of and behind a tile's sum 4, 5.3 (7.5) and
+  // 10.5 us; a split costs a second launch (4 us) and its partial sums' way to
+  // memory and back (at 4 TB/s), an operand that is packed first a launch behind
+  // others (2.5 us) and as much.  Over 160 random products the way chosen took
+  // 1.01 times the time of the best tiling and split (geometric mean).
   struct Way {
     int tile, groups, splits, direct;
     double us;
@@ -84,34 +85,36 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
   auto way = [&](int tile, int groups) {
     const int64_t all = tiles(tile), slots = tile == 128 && groups == 1 ? 512 : 256, rest = all % slots;
     const int64_t each = (stages + groups - 1) / groups;  // a group's stages
-    const double stage_us = tile == 256 ? 1.0 : tile == 128 ? 0.6 : i8 ? 0.3 : 0.55;
-    Way w = {tile, groups, 1, (int)all, stage_us * (double)each};
+    const bool off = i8 && (off_q || off_p);
+    const double stage_us = tile == 256   ? (i8 ? 0.75 : 0.85)
+                            : tile == 128 ? (off ? 0.8 : i8 ? 0.55 : 0.6)
+                                          : (off ? 0.5 : i8 ? 0.3 : 0.55);
+    const double ends_us = tile == 256 ? 10.5 : tile == 128 ? (off ? 7.5 : 5.3) : 4.0;
+    const double whole = (double)(all / slots) * (stage_us * (double)each + ends_us);
+    Way w = {tile, groups, 1, (int)all, whole + (rest > 0 ? stage_us * (double)each + ends_us : 0.0)};
     const double tile_us = (double)tile * tile * 8 / 4e6;  // written and read
     const int64_t most = rest > 0 ? std::min<int64_t>({slots / rest, each / 4, 32}) : 1;
     for (int64_t n = 2; n <= most; ++n) {
-      const double us = stage_us * (double)((each + n - 1) / n) + 4.0 + tile_us * (double)(rest * n);
+      const double us = whole + stage_us * (double)((each + n - 1) / n) + ends_us + 4.0 + tile_us * (double)(rest * n);
       if (us < w.us) {
         w.us = us;
         w.splits = (int)n;
         w.direct = (int)(all - rest);
       }
     }
+    if (tile == 256)
+      w.us += (off_q ? 2.5 + (double)(a_rows * a_cols * sa) * 2 / 4e6 : 0.0) +
+              (off_p ? 2.5 + (double)(b_rows * b_cols) * 2 / 4e6 : 0.0);
     return w;
   };
-  // 256-wide tiles from three quarters of the compute units on.  Below, 64- or
-  // 128-wide ones that are at most one per unit, with wave groups sharing K,
-  // whichever is faster by the above (integer product of 300 x 2880 from 1408:
-  // 64-wide 6.6 us, 128-wide 11.5; input gradient of 128 x 3584 from 18944:
-  // 60 and 36); else 128-wide ones with one group.
-  Way w;
-  if (tiles(256) >= 192) {
-    w = way(256, 1);
-  } else {
-    w = way(128, tiles(128) <= 256 ? 2 : 1);
-    if (tiles(64) <= 256) {
-      const Way small = way(64, 4);
-      if (small.us < w.us) w = small;
-    }
+  // (wave groups that share K need a compute unit of their own: as many tiles
+  // at most)
+  Way w = way(128, tiles(128) <= 256 ? 2 : 1);
+  const Way large = way(256, 1);
+  if (large.us < w.us) w = large;
+  if (tiles(64) <= 256) {
+    const Way small = way(64, 4);
+    if (small.us < w.us) w = small;
   }
   c.tile = w.tile;
   c.groups = w.groups;
