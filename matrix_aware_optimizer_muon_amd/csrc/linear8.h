@@ -81,11 +81,15 @@ struct MmParams {
 
 hipError_t launch_mm(const MmParams& p, ProductKind kind, hipStream_t s);
 
-// The product for few rows of x (generated tokens, short batches; at most
-// 64): no tiles, no alignment, reads the weights once.  From 33 rows on the
-// reads of x count as well: measured against the tile kernel at 64 rows, 10
-// against 15 us for 4000 x 4000 weights, 32 against 27 us for 18944 x 3584.
-inline bool few_rows(int64_t t, int64_t n, int64_t k) { return t <= 32 || (t <= 64 && n * k <= 1 << 25); }
+// The product for few rows of x (generated tokens, short batches): no tiles,
+// no alignment, reads the weights once.  Up to 16 rows it loses to tiles that
+// share K where K is long and there are few workgroups (one row, 16384 x 16384
+// weights 40 and 44 us, 1024 x 8192 7.4 and 10.2, 1024 x 65536 69 and 22); up
+// to 32 the reads of x count as well (32 rows, 2048 x 4096: 7.9 and 9.8,
+// 2048 x 8192 13.0 and 11.5, 18944 x 3584 27 and 25).
+inline bool few_rows(int64_t t, int64_t n, int64_t k) {
+  return t <= 16 ? k <= 8192 || n >= 16384 : t <= 32 && k <= 4096 && n * k <= 1 << 24;
+}
 hipError_t launch_few(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw,
                       const float* ws, void* y, int64_t ldy, bool bf16, int t, int n, int k, hipStream_t s);
 

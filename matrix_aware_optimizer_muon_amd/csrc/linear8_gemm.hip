@@ -741,46 +741,39 @@ __global__ void __launch_bounds__(256) mm_sum_kernel(const MmParams p) {
   put4(p, (int64_t)r * p.ldo + c, n, v);
 }
 
-// Few rows of x (at most 16 QB).  A workgroup takes 16 PB rows of w; its four
-// waves take every fourth 64-byte step of K, straight from memory into MFMA
-// fragments at any alignment (a row of w is read once, by one workgroup; x
-// comes from the caches), and the int32 partial tiles are added through LDS.
-// Bound by the read of w: one row of x against 18944 x 3584 takes 12.1 us,
-// 5.6 TB/s.
-template <int PB, int QB>
-__global__ void __launch_bounds__(256) few_kernel(const int8_t* xq, int64_t ldx, const float* xs,
+// Few rows of x (at most 16 QB).  A workgroup takes 16 rows of w; its W waves
+// take every W-th 64-byte step of K, straight from memory into MFMA fragments
+// at any alignment (a row of w is read once, by one workgroup; x comes from
+// the caches), and the int32 partial tiles are added through LDS.  Bound by
+// the read of w: one row of x against 18944 x 3584 takes 12.1 us, 5.6 TB/s.
+template <int QB, int W>
+__global__ void __launch_bounds__(64 * W) few_kernel(const int8_t* xq, int64_t ldx, const float* xs,
                                                   const int8_t* wq, int64_t ldw, const float* ws, void* y,
                                                   int64_t ldy, int bf16, int t, int n, int k) {
-  __shared__ i32x4 s_part[3][PB * QB][64];
+  __shared__ i32x4 s_part[W - 1][QB][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int q4 = lane >> 4, c16 = lane & 15;
-  const int n0 = blockIdx.x * (16 * PB);
-  const int8_t *wr[PB], *xr[QB];
-#pragma unroll
-  for (int i = 0; i < PB; ++i) wr[i] = wq + (int64_t)min(n0 + 16 * i + c16, n - 1) * ldw + q4 * 16;
+  const int n0 = blockIdx.x * 16;
+  const int8_t* const wr = wq + (int64_t)min(n0 + c16, n - 1) * ldw + q4 * 16;
+  const int8_t* xr[QB];
 #pragma unroll
   for (int j = 0; j < QB; ++j) xr[j] = xq + (int64_t)min(16 * j + c16, t - 1) * ldx + q4 * 16;
-  i32x4 acc[PB][QB];
+  i32x4 acc[QB];
 #pragma unroll
-  for (int i = 0; i < PB; ++i)
-#pragma unroll
-    for (int j = 0; j < QB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  for (int j = 0; j < QB; ++j) acc[j] = i32x4{0, 0, 0, 0};
   const int whole = k / 64;
   int s = wave;
 #pragma unroll 4
-  for (; s < whole; s += 4) {
-    u32x4 a[PB], b[QB];
-#pragma unroll
-    for (int i = 0; i < PB; ++i) __builtin_memcpy(&a[i], wr[i] + s * 64, 16);
+  for (; s < whole; s += W) {
+    u32x4 a, b[QB];
+    __builtin_memcpy(&a, wr + s * 64, 16);
 #pragma unroll
     for (int j = 0; j < QB; ++j) __builtin_memcpy(&b[j], xr[j] + s * 64, 16);
 #pragma unroll
-    for (int i = 0; i < PB; ++i)
-#pragma unroll
-      for (int j = 0; j < QB; ++j) Mfma<true>::go(a[i], b[j], acc[i][j]);
+    for (int j = 0; j < QB; ++j) Mfma<true>::go(a, b[j], acc[j]);
   }
   if (s == whole && k % 64) {  // one wave takes the ragged last step
-    u32x4 a[PB], b[QB];
+    u32x4 a, b[QB];
     const int left = k - whole * 64 - q4 * 16;
     auto part = [&](const int8_t* r, const int8_t* base, int64_t total) {
       const char* c = (const char*)r + whole * 64;
@@ -791,30 +784,28 @@ __global__ void __launch_bounds__(256) few_kernel(const int8_t* xq, int64_t ldx,
         if (i < left) v[i / 4] |= (uint32_t)(uint8_t)c[i] << (8 * (i % 4));
       return v;
     };
-#pragma unroll
-    for (int i = 0; i < PB; ++i) a[i] = part(wr[i], wq, (int64_t)(n - 1) * ldw + k);
+    a = part(wr, wq, (int64_t)(n - 1) * ldw + k);
 #pragma unroll
     for (int j = 0; j < QB; ++j) b[j] = part(xr[j], xq, (int64_t)(t - 1) * ldx + k);
 #pragma unroll
-    for (int i = 0; i < PB; ++i)
-#pragma unroll
-      for (int j = 0; j < QB; ++j) Mfma<true>::go(a[i], b[j], acc[i][j]);
+    for (int j = 0; j < QB; ++j) Mfma<true>::go(a, b[j], acc[j]);
   }
   if (wave > 0) {
 #pragma unroll
-    for (int i = 0; i < PB * QB; ++i) s_part[wave - 1][i][lane] = acc[i / QB][i % QB];
+    for (int j = 0; j < QB; ++j) s_part[wave - 1][j][lane] = acc[j];
   }
   __syncthreads();
   if (wave > 0) return;
   MmParams p = {};
   p.out = y;
   p.obf16 = bf16;
+  const int c = n0 + 4 * q4;
 #pragma unroll
-  for (int i = 0; i < PB * QB; ++i) {
-    i32x4 a = acc[i / QB][i % QB];
+  for (int j = 0; j < QB; ++j) {
+    i32x4 a = acc[j];
 #pragma unroll
-    for (int q = 0; q < 3; ++q) a += s_part[q][i][lane];
-    const int c = n0 + 16 * (i / QB) + 4 * q4, r = 16 * (i % QB) + c16;
+    for (int q = 0; q < W - 1; ++q) a += s_part[q][j][lane];
+    const int r = 16 * j + c16;
     if (c < n && r < t) {
       const float sx = xs[r];
       float v[4];
@@ -878,16 +869,16 @@ hipError_t launch_mm(const MmParams& p, ProductKind kind, hipStream_t s) {
 
 hipError_t launch_few(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw,
                       const float* ws, void* y, int64_t ldy, bool bf16, int t, int n, int k, hipStream_t s) {
-  auto go = [&](auto kernel, int rows) {
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)((n + rows - 1) / rows)), dim3(256), 0, s, xq, ldx, xs, wq, ldw,
-                       ws, y, ldy, bf16 ? 1 : 0, t, n, k);
+  auto go = [&](auto kernel, int waves) {
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)((n + 15) / 16)), dim3(64 * waves), 0, s, xq, ldx, xs, wq, ldw, ws, y,
+                       ldy, bf16 ? 1 : 0, t, n, k);
     return hipGetLastError();
   };
-  // two blocks of w's rows per workgroup halve the reads of x; with fewer than
-  // 256 workgroups left they would leave compute units without one
-  if (t <= 16) return go(few_kernel<1, 1>, 16);
-  if (t > 32) return go(few_kernel<1, 4>, 16);
-  return n >= 256 * 32 ? go(few_kernel<2, 2>, 32) : go(few_kernel<1, 2>, 16);
+  // Eight waves read a row's K faster than four until there are four
+  // workgroups per compute unit (8192 x 8192: 14.5 and 21.9 us; 18944 x 3584:
+  // 16 and 14).
+  if (t > 16) return go(few_kernel<2, 8>, 8);
+  return n < 16 * 1024 ? go(few_kernel<1, 8>, 8) : go(few_kernel<1, 4>, 4);
 }
 
 hipError_t launch_pack(const void* src, int64_t lds, int64_t bytes, void* dst, int64_t ld, int64_t rows,

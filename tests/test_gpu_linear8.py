@@ -298,6 +298,12 @@ def test_matmul_few_rows(t, n, k, dtype):
     check_matmul(t, n, k, dtype)
 
 
+@pytest.mark.parametrize("t, n, k", [(1, 40, 8192), (16, 40, 8193), (2, 3, 30001), (32, 50, 4096), (17, 50, 4100),
+                                     (32, 4097, 4095), (5, 16383, 70), (16, 16385, 130), (31, 70, 20000)])
+def test_matmul_few_rows_either_side_of_their_rules(t, n, k):
+    check_matmul(t, n, k, F32)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("t, n, k", [(65, 1, 16), (100, 8, 33), (128, 128, 64), (129, 127, 80), (300, 130, 512),
                                      (257, 400, 1), (96, 64, 48), (95, 513, 100), (72, 260, 4096), (130, 130, 8191),
