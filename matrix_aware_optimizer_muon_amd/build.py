@@ -58,7 +58,7 @@ def build_binding(verbose: bool = False) -> str:
            "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(rocm, "include"),
            os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L", lib, "-L", PKG, "-lmuon", "-ltorch_python",
-           "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+           "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{BINDING_SOURCE} failed:\n{r.stdout}\n{r.stderr}")

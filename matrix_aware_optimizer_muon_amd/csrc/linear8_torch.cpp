@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
@@ -111,8 +112,10 @@ void same(const at::Tensor& t, const at::Tensor& x, const char* what, const char
     bad(std::string(what) + " must have " + as + "'s shape and type");
 }
 
+// (past the dispatcher: at::empty took 0.25 us more, four times for a norm to
+// 8 bits, 6.2 -> 5.2 us a call)
 at::Tensor make(at::IntArrayRef size, at::ScalarType t, const at::Tensor& like) {
-  return at::empty(size, at::TensorOptions().dtype(t).device(like.device()));
+  return at::Tensor(at::detail::empty_cuda(size, t, like.device(), std::nullopt));
 }
 at::IntArrayRef leading(const at::Tensor& t) { return t.sizes().slice(0, t.dim() - 1); }
 
