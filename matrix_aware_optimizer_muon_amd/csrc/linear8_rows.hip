@@ -517,7 +517,13 @@ __global__ void __launch_bounds__(1024) norm_back_sum_kernel(const float* part, 
   const int64_t c = (int64_t)blockIdx.x * 16 + cl;
   float a = 0.0f;
   if (c < cols)
-    for (int g = g0; g < groups; g += 64) a += part[(int64_t)g * cols + c];
+    for (int g = g0; g < groups; g += 256) {  // four reads in flight
+      float v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = part[(int64_t)min(g + 64 * u, groups - 1) * cols + c];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) a += g + 64 * u < groups ? v[u] : 0.0f;
+    }
   s[g0][cl] = a;
   __syncthreads();
 #pragma unroll
