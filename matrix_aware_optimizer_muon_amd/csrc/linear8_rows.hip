@@ -15,6 +15,8 @@
 // the division and the restored value q * scale exact, so rint is the only
 // rounding (at most scale / 2), and lets the gradient products fold the scale
 // into a bf16 operand without rounding.
+#include <algorithm>
+
 #include "common.hpp"
 #include "linear8.h"
 
@@ -632,12 +634,15 @@ hipError_t launch_norm(const NormParams& p, bool bf16, hipStream_t s) {
 // 54 / 60 / 66 at 8192; from 8-bit rows without dh: 52 / 37 / 33 / 41, 59 / 41
 // / 37 / 48 and 40 / 45 / 51 / 56.  Fp32 rows (twice the bytes in flight) and
 // short batches do better with 512 (f32, 8192 x 3584, dh: 90 against 107; bf16,
-// 2048 x 4096: 21 against 24).
+// 2048 x 4096: 21 against 24).  Between, rows of over 1024 columns come two or
+// four to a workgroup, so that the partial rows stay fewer than the rows (512 x
+// 3584: 10.8 us with 256 groups, 13.2 with 512; 1024 x 3584: 13.8 and 15.0).
 int norm_back_groups(int64_t rows, int64_t cols, bool bf16) {
   const int64_t side = cols <= 128 ? 32 : cols <= 256 ? 16 : cols <= 512 ? 8 : cols <= 1024 ? 4 : 1;  // RPB
   const int64_t need = (rows + side - 1) / side;
   const int64_t full = cols > 4096 ? 256 : bf16 && need >= 4096 ? 768 : 512;
-  return (int)(need < full ? need : full);
+  if (side > 1 || need <= 128) return (int)std::min(need, full);
+  return (int)std::min(full, std::max({(int64_t)128, std::min<int64_t>((need + 1) / 2, 256), (need + 3) / 4}));
 }
 
 hipError_t launch_norm_back(const NormBackParams& p, bool bf16, hipStream_t s) {
