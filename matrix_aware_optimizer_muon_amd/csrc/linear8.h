@@ -23,6 +23,7 @@ struct NormParams {
   float* scale;
   float* rstd;
   int64_t rows, cols;
+  int64_t row0;        // the launch's first row (set at the launch)
   int64_t ldx, ldr, ldh, ldy, ldq;
   double eps;
 };

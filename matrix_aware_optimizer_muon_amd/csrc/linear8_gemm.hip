@@ -844,13 +844,15 @@ hipError_t go_mm(const MmParams& p, hipStream_t s) {
   const int T = p.tile;
   const int64_t tiles = (int64_t)((p.np + T - 1) / T) * ((p.nq + T - 1) / T), rest = tiles - p.direct;
   const int64_t blocks = p.direct + rest * p.splits;
-  if (blocks > 0x7fffffff || rest < 0 || (T == 256 && p.unaligned)) return hipErrorInvalidValue;
+  // (a launch has fewer than 2^32 threads; outputs that need more pass any memory)
+  const int threads = 64 * waves_of(T) * p.groups;
+  if (blocks > 0xffffffffll / threads || rest < 0 || (T == 256 && p.unaligned)) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)blocks);
-  auto go = [&](auto kernel, int waves) { hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, s, p); };
-  if (T == 256) go(mm_kernel<KIND, false, 256, 1>, 8);
-  else if (T == 128 && p.groups == 2) p.unaligned ? go(mm_kernel<KIND, true, 128, 2>, 8) : go(mm_kernel<KIND, false, 128, 2>, 8);
-  else if (T == 128) p.unaligned ? go(mm_kernel<KIND, true, 128, 1>, 4) : go(mm_kernel<KIND, false, 128, 1>, 4);
-  else p.unaligned ? go(mm_kernel<KIND, true, 64, 4>, 16) : go(mm_kernel<KIND, false, 64, 4>, 16);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, p); };
+  if (T == 256) go(mm_kernel<KIND, false, 256, 1>);
+  else if (T == 128 && p.groups == 2) p.unaligned ? go(mm_kernel<KIND, true, 128, 2>) : go(mm_kernel<KIND, false, 128, 2>);
+  else if (T == 128) p.unaligned ? go(mm_kernel<KIND, true, 128, 1>) : go(mm_kernel<KIND, false, 128, 1>);
+  else p.unaligned ? go(mm_kernel<KIND, true, 64, 4>) : go(mm_kernel<KIND, false, 64, 4>);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 sums((uint32_t)(T * T / 1024), (uint32_t)rest);

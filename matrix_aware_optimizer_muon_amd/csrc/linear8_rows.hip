@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p)
   __shared__ double s_sum[W];
   __shared__ uint32_t s_top[W];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, at = threadIdx.x % LPR;
-  const int64_t row = (int64_t)blockIdx.x * RW::RPB + threadIdx.x / LPR;
+  const int64_t row = p.row0 + (int64_t)blockIdx.x * RW::RPB + threadIdx.x / LPR;
   if (row >= p.rows) return;  // RPB > 1 only, which has no barrier below
   const int cols = (int)p.cols;
   const int c0 = at * 8;
@@ -537,15 +537,15 @@ __global__ void __launch_bounds__(1024) norm_back_sum_kernel(const float* part, 
 }
 
 // x = q * scale.  The matrix is cut into chunks of 16 stored bytes (8 bf16 or 4
-// fp32 columns), one per thread.
+// fp32 columns), one per thread, from chunk `first` on.
 template <typename T>
 __global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* q, int64_t ldq, const float* scale,
                                                          typename Elem<T>::type* x, int64_t ldx, int64_t rows,
-                                                         int cols) {
+                                                         int cols, int64_t first) {
   typedef typename Elem<T>::type E;
   constexpr int C = 16 / sizeof(E);
   const uint32_t cpr = (uint32_t)(cols + C - 1) / C;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t id = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = id >> 32 ? id / cpr : (int64_t)((uint32_t)id / cpr);
   if (row >= rows) return;
   const int col = (int)(id - row * cpr) * C, n = cols - col;
@@ -567,12 +567,27 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* q, int64_
   }
 }
 
+// Calls launch(first block, blocks) until all are out.  A launch has fewer than
+// 2^32 threads: given more, the runtime drops the upper bits of their number,
+// runs what is left and reports no error.
+template <typename F>
+hipError_t in_launches(int64_t blocks, int threads, F launch) {
+  const int64_t most = 0xffffffffll / threads;
+  hipError_t e = hipSuccess;
+  for (int64_t b = 0; b < blocks && e == hipSuccess; b += most) {
+    launch(b, (uint32_t)std::min(blocks - b, most));
+    e = hipGetLastError();
+  }
+  return e;
+}
+
 template <typename T, int MODE, bool RES, int LPR, int NC>
-hipError_t go_norm(const NormParams& p, hipStream_t s) {
+hipError_t go_norm(NormParams p, hipStream_t s) {
   typedef Rows<LPR> RW;
-  const int64_t blocks = (p.rows + RW::RPB - 1) / RW::RPB;
-  hipLaunchKernelGGL((norm_kernel<T, MODE, RES, LPR, NC>), dim3((uint32_t)blocks), dim3(RW::NT), 0, s, p);
-  return hipGetLastError();
+  return in_launches((p.rows + RW::RPB - 1) / RW::RPB, RW::NT, [&](int64_t first, uint32_t blocks) {
+    p.row0 = first * RW::RPB;
+    hipLaunchKernelGGL((norm_kernel<T, MODE, RES, LPR, NC>), dim3(blocks), dim3(RW::NT), 0, s, p);
+  });
 }
 
 // Lanes and chunks by width: the fewest lanes that hold the row in two chunks
@@ -671,16 +686,15 @@ hipError_t launch_quantize(const void* x, int64_t ldx, int8_t* q, int64_t ldq, f
 
 hipError_t launch_dequantize(const int8_t* q, int64_t ldq, const float* scale, void* x, int64_t ldx,
                              int64_t rows, int64_t cols, bool bf16, hipStream_t s) {
-  const int64_t per = bf16 ? 8 : 4, blocks = (rows * ((cols + per - 1) / per) + 255) / 256;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid((uint32_t)blocks);
-  if (bf16)
-    hipLaunchKernelGGL(dequantize_kernel<BF16>, grid, dim3(256), 0, s, q, ldq, scale, (uint16_t*)x, ldx, rows,
-                       (int)cols);
-  else
-    hipLaunchKernelGGL(dequantize_kernel<F32>, grid, dim3(256), 0, s, q, ldq, scale, (float*)x, ldx, rows,
-                       (int)cols);
-  return hipGetLastError();
+  const int64_t per = bf16 ? 8 : 4;
+  return in_launches((rows * ((cols + per - 1) / per) + 255) / 256, 256, [&](int64_t first, uint32_t blocks) {
+    if (bf16)
+      hipLaunchKernelGGL(dequantize_kernel<BF16>, dim3(blocks), dim3(256), 0, s, q, ldq, scale, (uint16_t*)x, ldx,
+                         rows, (int)cols, first * 256);
+    else
+      hipLaunchKernelGGL(dequantize_kernel<F32>, dim3(blocks), dim3(256), 0, s, q, ldq, scale, (float*)x, ldx, rows,
+                         (int)cols, first * 256);
+  });
 }
 
 }  // namespace l8
