@@ -53,9 +53,9 @@ extern "C" {
  * residual is NULL); rstd = 1 / sqrt(mean(h^2) + eps) per row;
  * y = h * rstd * weight.  Exactly one of y and q is given: y takes rows of
  * the type, q and scale the 8-bit form of the unrounded y.  The sum of
- * squares, rstd and the 8-bit rounding are carried in 64 bits, so q does not
- * depend on how a row is split over the hardware.  (A row for which
- * |h * weight| passes fp32's range counts as non-finite in 8 bits.)
+ * squares, rstd, the 8-bit scale and rounding are carried in 64 bits, so q
+ * does not depend on how a row is split over the hardware.  (A row whose
+ * largest |y| passes fp32's range counts as non-finite in 8 bits.)
  * eps >= 0. */
 muon_status muon_rmsnorm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                                  const float* weight, muon_dtype dtype, int64_t rows, int64_t cols,

@@ -141,10 +141,10 @@ __device__ __forceinline__ void store8(E* p, int n, const E e[8]) {
 }
 
 // Over aligned groups of L lanes of a wave.
-template <int L>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+template <int L, typename V>
+__device__ __forceinline__ V lanes_max(V v) {
 #pragma unroll
-  for (int off = L / 2; off > 0; off >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, off, 64));
+  for (int off = L / 2; off > 0; off >>= 1) v = max(v, __shfl_xor(v, off, 64));
   return v;
 }
 template <int L, typename V>
@@ -166,12 +166,32 @@ struct Rows {
   static constexpr bool JOIN = W > 1;
 };
 
+// Magnitudes as bits, whose order is theirs, with infinity and NaN on top: a
+// row's values in 32 bits, products of two of them in 64, where they are exact.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint64_t magnitude(double v) {
+  return (uint64_t)__double_as_longlong(v) & 0x7fffffffffffffffull;
+}
+
 // Biased exponent of the scale for a row whose largest magnitude has the
 // bits `top` (finite): 127 = 1.984375 * 2^6, so 127 * 2^e >= top needs
 // e = E - 6, one more if top's mantissa exceeds 1.984375's.
 __device__ __forceinline__ uint32_t scale_field(uint32_t top) {
   const int f = (int)(top >> 23) - 6 + ((top & 0x7fffffu) > 0x7e0000u ? 1 : 0);
   return (uint32_t)max(f, 1);
+}
+__device__ __forceinline__ uint32_t scale_field(uint64_t top) {
+  const int f = (int)(top >> 52) - (1023 - 127) - 6 + ((top & 0xfffffffffffffull) > 0xfc00000000000ull ? 1 : 0);
+  return (uint32_t)max(f, 1);
+}
+
+// Whether y = top * rstd, top a row's largest |h w| as rounded in fp32, may
+// have another scale than the unrounded one: where top is under 2^-120 (its
+// rounding may be of any size), where y comes near fp32's end (infinities and
+// NaN among them), and within 2^-22 of 127 * 2^e (rounding moves y by 2^-24).
+__device__ __forceinline__ bool in_doubt(uint32_t top, double y) {
+  const int64_t from = (int64_t)(magnitude(y) & 0xfffffffffffffull) - 0xfc00000000000ll;
+  return top < 7u << 23 || !(y < 0x1p127) || (from < 1ll << 31 && from > -(1ll << 31));
 }
 
 // MODE 0: quantize x; 1: norm to T; 2: norm to 8 bits.  LPR lanes per row, NC
@@ -182,7 +202,10 @@ __device__ __forceinline__ uint32_t scale_field(uint32_t top) {
 // scale)) is taken in 64 bits too: a value next to a rounding border then
 // rounds as the formula's does, whatever order the row was summed in.  Each
 // lane's 64-bit operations (five per element) run at the fp32 rate on this
-// part and hide behind the row's loads.
+// part and hide behind the row's loads.  The scale follows from the largest
+// |h w|, found in fp32, where that leaves no doubt (`in_doubt`); rows where it
+// does find it again in 64 bits (doing so for every row took 8192 x 3584 bf16,
+// no residual, from 28.0 to 32.5 us, 1500 x 18944 from 37.8 to 44.4).
 template <typename T, int MODE, bool RES, int LPR, int NC>
 __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p) {
   typedef typename Elem<T>::type E;
@@ -190,6 +213,7 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p)
   constexpr int W = RW::JOIN ? RW::W : 1;
   __shared__ double s_sum[W];
   __shared__ uint32_t s_top[W];
+  __shared__ uint64_t s_exact[W];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, at = threadIdx.x % LPR;
   const int64_t row = p.row0 + (int64_t)blockIdx.x * RW::RPB + threadIdx.x / LPR;
   if (row >= p.rows) return;  // RPB > 1 only, which has no barrier below
@@ -243,7 +267,7 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p)
   }
 
   double sum = 0.0;
-  uint32_t top = 0;  // largest |v| (|h w| for MODE 2) as bits: NaN stays on top
+  uint32_t top = 0;  // largest |v| (|h w| for MODE 2)
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     if (c0 + i * STEP < cols) {
@@ -255,8 +279,8 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p)
           const double d = (double)v[i][j];
           sum = __builtin_fma(d, d, sum);
         }
-        if constexpr (MODE == 0) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
-        if constexpr (MODE == 2) top = max(top, __float_as_uint(v[i][j] * w[j]) & 0x7fffffffu);
+        if constexpr (MODE == 0) top = max(top, magnitude(v[i][j]));
+        if constexpr (MODE == 2) top = max(top, magnitude(v[i][j] * w[j]));
       }
     }
   }
@@ -297,9 +321,34 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p)
       }
     }
   } else {
-    if constexpr (MODE == 2) top = __float_as_uint((float)((double)__uint_as_float(top) * rstd)) & 0x7fffffffu;
-    const bool finite = top < 0x7f800000u;
-    const uint32_t f = finite ? scale_field(top) : 127u;
+    bool finite = top < 0x7f800000u;
+    uint32_t f = scale_field(top);
+    if constexpr (MODE == 2) {
+      double y = (double)__uint_as_float(top) * rstd;
+      if (in_doubt(top, y)) {  // the whole row's lanes
+        uint64_t exact = 0;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          if (c0 + i * STEP < cols) {
+            float w[8];
+            weights(i, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) exact = max(exact, magnitude((double)v[i][j] * (double)w[j]));
+          }
+        }
+        exact = lanes_max<RW::L>(exact);
+        if constexpr (RW::JOIN) {
+          if (lane == 0) s_exact[wave] = exact;
+          __syncthreads();
+#pragma unroll
+          for (int k = 0; k < W; ++k) exact = max(exact, s_exact[k]);
+        }
+        y = __longlong_as_double((long long)exact) * rstd;
+      }
+      finite = magnitude((float)y) < 0x7f800000u;
+      f = scale_field(magnitude(y));
+    }
+    f = finite ? f : 127u;
     const float inv = __uint_as_float((254u - f) << 23);  // 2^-e; f <= 249, so never subnormal
     if (at == 0)
       p.scale[row] = finite ? __uint_as_float(f << 23) : __uint_as_float(0x7fc00000u);
