@@ -14,6 +14,8 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
@@ -119,6 +121,19 @@ at::Tensor make(at::IntArrayRef size, at::ScalarType t, const at::Tensor& like) 
 }
 at::IntArrayRef leading(const at::Tensor& t) { return t.sizes().slice(0, t.dim() - 1); }
 
+// What a forward operator leaves for autograd, if it records and an input
+// requires a gradient: a node that raises when a backward pass reaches it.  Of
+// 8-bit rows the scale carries it.  (The backward operators leave nothing:
+// their results are gradients already.)
+template <typename... In> std::shared_ptr<torch::autograd::Node> undifferentiated(const char* name, const In&... in) {
+  using namespace torch::autograd;
+  if (!compute_requires_grad(in...)) return nullptr;
+  return std::shared_ptr<Node>(new NotImplemented(name, collect_next_edges(in...)), deleteNode);
+}
+void mark(const at::Tensor& out, const std::shared_ptr<torch::autograd::Node>& node) {
+  if (node) torch::autograd::set_history(out, node);
+}
+
 hipStream_t stream(const at::Tensor& t) {
   return c10::hip::getCurrentHIPStream(t.device().index()).stream();
 }
@@ -154,6 +169,7 @@ PyObject* do_quantize(PyObject* const* a, Py_ssize_t n) {
   at::Tensor q = make(x.sizes(), at::kChar, x), scale = make(leading(x), at::kFloat, x);
   check(muon_q8_quantize(ptr(x), s.ld, t, s.r, s.c, ptr<int8_t>(q), s.c, ptr<float>(scale), stream(x)),
         "muon_q8_quantize");
+  mark(scale, undifferentiated("linear8.quantize", x));
   return wrap8(std::move(q), std::move(scale));
 }
 
@@ -169,6 +185,7 @@ PyObject* do_dequantize(PyObject* const* a, Py_ssize_t n) {
   check(muon_q8_dequantize(ptr<int8_t>(x.q), x.s.ld, ptr<float>(x.scale), x.s.r, x.s.c, ptr(out), x.s.c, t,
                            stream(x.q)),
         "muon_q8_dequantize");
+  mark(out, undifferentiated("linear8.dequantize", x.scale));
   return wrap(std::move(out));
 }
 
@@ -186,12 +203,14 @@ PyObject* do_rmsnorm(PyObject* const* a, Py_ssize_t n) {
   if (eight < 0) throw Raised();
   const void* res = nullptr;
   int64_t ldr = 0;
+  const at::Tensor* residual = nullptr;
   if (a[2] != Py_None) {
     const at::Tensor& r = tensor(a[2], "residual");
     same(r, x, "residual", "x");
     ldr = rows(r, "residual").ld;
     device(x, r);
     res = ptr(r);
+    residual = &r;
   }
   device(x);
   device(x, w);
@@ -207,6 +226,11 @@ PyObject* do_rmsnorm(PyObject* const* a, Py_ssize_t n) {
                              eight ? ptr<int8_t>(y) : nullptr, s.c, eight ? ptr<float>(scale) : nullptr,
                              ptr<float>(rstd), stream(x)),
         "muon_rmsnorm_forward");
+  if (const auto node = undifferentiated("linear8.rmsnorm", x, w, residual ? *residual : x)) {
+    mark(eight ? scale : y, node);
+    mark(rstd, node);
+    if (residual) mark(h, node);
+  }
   PyObject* first = eight ? wrap8(std::move(y), std::move(scale)) : wrap(std::move(y));
   if (!first) throw Raised();
   PyObject* second;
@@ -305,6 +329,7 @@ PyObject* do_matmul(PyObject* const* a, Py_ssize_t n) {
                        ptr<float>(w.scale), x.s.r, w.s.r, x.s.c, ptr(y), w.s.r, t, need ? ptr(ws) : nullptr,
                        need, stream(x.q)),
         "muon_q8_matmul");
+  mark(y, undifferentiated("linear8.matmul", x.scale, w.scale));
   return wrap(std::move(y));
 }
 

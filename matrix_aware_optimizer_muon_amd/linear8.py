@@ -12,9 +12,12 @@ An 8-bit tensor is a `Q8`: int8 rows and one power-of-two fp32 scale per row
 (value = q * scale).  Tensors are CUDA tensors with unit stride in the last
 dimension; 2-D ones may have any row stride, others are taken as rows of their
 last dimension and must be contiguous.  Forward and backward are calls of
-their own: nothing is recorded for autograd.  Work is enqueued on the current
-stream of the tensors' device; results and workspaces come from torch's
-allocator.  Argument errors raise ValueError, or MuonError from the C ABI.
+their own: nothing is recorded for autograd.  Where an input of a forward call
+requires a gradient, the results do too, and torch's backward pass through them
+raises; a torch.autograd.Function around the calls gives them a gradient.  Work
+is enqueued on the current stream of the tensors' device; results and
+workspaces come from torch's allocator.  Argument errors raise ValueError, or
+MuonError from the C ABI.
 
 The functions only forward to the compiled binding (csrc/linear8_torch.cpp),
 which checks, allocates and calls libmuon.so; there is no fallback.
