@@ -392,6 +392,7 @@ PyObject* do_grad_weight(PyObject* const* a, Py_ssize_t n) {
                             ptr(out), ldo, t, accumulate, need ? ptr(ws) : nullptr, need, stream(dy)),
         "muon_q8_grad_weight");
   if (a[3] != Py_None) {
+    if (!out.is_inference()) torch::autograd::impl::bump_version(out);  // (autograd sees the write)
     Py_INCREF(a[3]);
     return a[3];
   }

@@ -87,3 +87,20 @@ def test_the_backward_operators_give_constants():
     assert not l8.grad_input(dy, w8).requires_grad and not l8.grad_weight(dy, x8).requires_grad
     y, h, rstd = l8.rmsnorm(x, leaf(48))
     assert not any(t.requires_grad for t in l8.rmsnorm_backward(y, h, rstd, leaf(48)))
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_writing_into_out_counts_as_a_write(accumulate):
+    x = l8.quantize(torch.randn(20, 48, device="cuda"))
+    dy = torch.randn(20, 32, device="cuda").bfloat16()
+    out = torch.ones(32, 48, device="cuda")
+    factor = leaf(32, 48)
+    loss = (factor * out).sum()  # keeps out for factor's gradient
+    before = out._version
+    assert l8.grad_weight(dy, x, out=out, accumulate=accumulate) is out
+    assert out._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():  # such tensors have no version
+        fresh = torch.zeros(32, 48, device="cuda")
+        assert torch.equal(l8.grad_weight(dy, x, out=fresh), l8.grad_weight(dy, x))
