@@ -101,3 +101,10 @@ hipError_t launch_pack(const void* src, int64_t lds, int64_t bytes, void* dst, i
 
 }  // namespace l8
 }  // namespace muon
+
+// How a product of these arguments runs (muon_q8_product), so that tests can
+// see which kernels their sizes reach; not part of the ABI.  out: few rows'
+// kernel, tile, wave groups, unaligned, operands a and b laid out again, tiles
+// of one workgroup, tiles that are split, their splits, stages of the whole sum.
+extern "C" void muon_l8_choice(int product, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t t,
+                               int64_t n, int64_t k, int64_t* out);

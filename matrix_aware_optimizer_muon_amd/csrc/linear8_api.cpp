@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <iterator>
 
 #include "linear8.h"
 #include "muon_linear8.h"
@@ -338,6 +339,16 @@ muon_status muon_q8_workspace(muon_q8_product product, const void* a, int64_t ld
   if (bad != MUON_OK) return bad;
   *workspace_bytes = (size_t)choose(product, a, lda, b, ldb, t, n, k).bytes;
   return MUON_OK;
+}
+
+// (linear8.h)
+void muon_l8_choice(int product, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t t, int64_t n,
+                    int64_t k, int64_t* out) {
+  const Choice c = choose((muon_q8_product)product, a, lda, b, ldb, t, n, k);
+  const int64_t T = c.tile, stages = (c.kd + (product == MUON_Q8_MATMUL ? 63 : 31)) / (product == MUON_Q8_MATMUL ? 64 : 32);
+  const int64_t tiles = c.few ? 0 : (c.np + T - 1) / T * ((c.nq + T - 1) / T);
+  const int64_t v[] = {c.few, T, c.groups, c.unaligned, c.pack_q, c.pack_p, c.direct, tiles - c.direct, c.splits, stages};
+  std::copy(std::begin(v), std::end(v), out);
 }
 
 muon_status muon_q8_matmul(const int8_t* xq, int64_t ldx, const float* x_scale, const int8_t* wq,
