@@ -51,7 +51,8 @@ extern "C" {
 
 /* h = x + residual rounded to the type (h = x and the h argument unused if
  * residual is NULL); rstd = 1 / sqrt(mean(h^2) + eps) per row;
- * y = h * rstd * weight.  Exactly one of y and q is given: y takes rows of
+ * y = h * rstd * weight, also where rstd itself is outside fp32's normal
+ * numbers (rms of h over 2^126 or under 2^-128).  Exactly one of y and q is given: y takes rows of
  * the type, q and scale the 8-bit form of the unrounded y.  The sum of
  * squares, rstd, the 8-bit scale and rounding are carried in 64 bits, so q
  * does not depend on how a row is split over the hardware.  (A row whose

@@ -306,7 +306,9 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p)
     if (at == 0) p.rstd[row] = (float)rstd;
   }
   if constexpr (MODE == 1) {
+    // (outside fp32's normal numbers r loses what y needs: all 64 bits there)
     const float r = (float)rstd;
+    const bool normal = magnitude(r) >= 1u << 23 && magnitude(r) < 0x7f800000u;
     E* y = (E*)p.y + row * p.ldy;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -317,6 +319,10 @@ __global__ void __launch_bounds__(Rows<LPR>::NT) norm_kernel(const NormParams p)
         weights(i, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) e[j] = Elem<T>::from(v[i][j] * r * w[j]);
+        if (!normal) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = Elem<T>::from((float)((double)v[i][j] * rstd * (double)w[j]));
+        }
         store8<true>(y + c, cols - c, e);
       }
     }
