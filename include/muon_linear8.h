@@ -93,7 +93,8 @@ muon_status muon_q8_workspace(muon_q8_product product, const void* a, int64_t ld
                               int64_t ldb, int64_t t, int64_t n, int64_t k, size_t* workspace_bytes);
 
 /* y[t][n] = x_scale[t] * w_scale[n] * sum_k xq[t][k] * wq[n][k]; the sum is
- * exact (int32), then scaled in fp32 and rounded to the type. */
+ * exact (int32), then scaled in fp32, by x_scale first (past 2^97 that may
+ * overflow though w_scale would bring it back), and rounded to the type. */
 muon_status muon_q8_matmul(const int8_t* xq, int64_t ldx, const float* x_scale, const int8_t* wq,
                            int64_t ldw, const float* w_scale, int64_t t, int64_t n, int64_t k, void* y,
                            int64_t ldy, muon_dtype dtype, void* workspace, size_t workspace_bytes,

@@ -83,11 +83,12 @@ struct MmParams {
 hipError_t launch_mm(const MmParams& p, ProductKind kind, hipStream_t s);
 
 // The product for few rows of x (generated tokens, short batches): no tiles,
-// no alignment, reads the weights once.  Against tiles that share K, in us: one
-// row, weights of 1024 x 8192 7.4 and 10.2, 18944 x 16384 56 and 75, but 1024 x
-// 65536 69 and 22 (few workgroups, long sums); up to 32 rows the reads of x
-// count as well: 32 rows, 2048 x 4096 7.9 and 9.8, 2048 x 8192 13.0 and 11.5,
-// 18944 x 3584 27 and 25.
+// no alignment, reads the weights once.  Against tiles that share K, weights
+// from memory, in us: one row, 18944 x 3584 13.8 and 23.0, 18944 x 16384 65 and
+// 80, 1024 x 8192 11.0 and 9.9 (6.9 and 9.0 where the last-level cache holds
+// them), but 1024 x 65536 68 and 22 (few workgroups, long sums); up to 32 rows
+// the reads of x count as well: 32 rows, 2048 x 4096 8.4 and 13.7, 2048 x 8192
+// 13.6 and 11.9, 18944 x 3584 31 and 25.
 inline bool few_rows(int64_t t, int64_t n, int64_t k) {
   return t <= 16 ? k <= 8192 || n >= 16384 : t <= 32 && k <= 4096 && n * k <= 1 << 24;
 }

@@ -37,7 +37,7 @@ muon_status row_sizes(int64_t rows, int64_t cols) {
 // How a product runs.  `few`: the kernel for few rows of x.
 struct Choice {
   bool few = false;
-  bool unaligned = false;          // read through registers (tile 128)
+  bool unaligned = false;          // read through registers (tiles 128 and 64)
   bool pack_q = false, pack_p = false;
   int64_t ldq = 0, ldp = 0;        // bytes, as the tile kernel reads them
   int padq = 0, padp = 0;          // readable after the last row
@@ -77,8 +77,7 @@ Choice choose(muon_q8_product kind, const void* a, int64_t lda, const void* b, i
   // in 256-wide ones; what is ahead of and behind a tile's sum 4, 5.3 (7.5) and
   // 10.5 us; a split costs a second launch (4 us) and its partial sums' way to
   // memory and back (at 4 TB/s), an operand that is packed first a launch behind
-  // others (2.5 us) and as much.  Over 160 random products the way chosen took
-  // 1.01 times the time of the best tiling and split (geometric mean).
+  // others (2.5 us) and as much.
   struct Way {
     int tile, groups, splits, direct;
     double us;

@@ -22,9 +22,10 @@
 // addresses, and never read).
 //
 // Bound by the matrix cores' issue and the card's power: a product of 4096 x
-// 18944 x 3584 takes 252 us (2.21 POP/s), the input gradient of that size 492
-// (1.13 PFLOP/s), the weight gradient 512 (1.09); the matrix cores are busy 59,
-// 58 and 50 % of the cycles, LDS 26 to 36 %, at 1.8 to 1.9 GHz.
+// 18944 x 3584 takes 242 to 252 us by the card (2.3 to 2.2 POP/s), the input
+// gradient of that size 479 to 492 (1.16 to 1.13 PFLOP/s), the weight gradient
+// 493 to 512 (1.13 to 1.09); the matrix cores are busy 59, 58 and 51 % of the
+// cycles, LDS 26 to 36 %, at 1.8 to 1.9 GHz.
 //
 // Ragged sizes: output rows and columns past the end re-read the last valid
 // one and are not stored; K past the end reads a zeroed line on both sides,
@@ -750,7 +751,8 @@ __global__ void __launch_bounds__(256) mm_sum_kernel(const MmParams p) {
 // take every W-th 64-byte step of K, straight from memory into MFMA fragments
 // at any alignment (a row of w is read once, by one workgroup; x comes from
 // the caches), and the int32 partial tiles are added through LDS.  Bound by
-// the read of w: one row of x against 18944 x 3584 takes 12.1 us, 5.6 TB/s.
+// the read of w: one row of x against 18944 x 3584 takes 13.9 us from memory
+// (4.9 TB/s) and 12.1 where the last-level cache holds w.
 template <int QB, int W>
 __global__ void __launch_bounds__(64 * W) few_kernel(const int8_t* xq, int64_t ldx, const float* xs,
                                                   const int8_t* wq, int64_t ldw, const float* ws, void* y,
@@ -882,8 +884,9 @@ hipError_t launch_few(const int8_t* xq, int64_t ldx, const float* xs, const int8
     return hipGetLastError();
   };
   // Eight waves read a row's K faster than four until there are four
-  // workgroups per compute unit (8192 x 8192: 14.5 and 21.9 us; 18944 x 3584:
-  // 16 and 14).
+  // workgroups per compute unit (one row of x, w from memory: 8192 x 8192 14.5
+  // and 21.4 us, 12000 x 8192 20.2 and 23.9, 16384 x 4096 15.8 and 15.7, 18944 x
+  // 3584 16.1 and 13.9).
   if (t > 16) return go(few_kernel<2, 8>, 8);
   return n < 16 * 1024 ? go(few_kernel<1, 8>, 8) : go(few_kernel<1, 4>, 4);
 }
