@@ -106,7 +106,8 @@ def _exponents(top):
 
 
 def _power(b):
-    return torch.ldexp(torch.ones_like(b, dtype=torch.float32), b.to(torch.int32) - 127)
+    """2^(b - 127) from its bits (1 <= b <= 254)."""
+    return (b.to(torch.int32) << 23).view(torch.float32)
 
 
 def _wide(s, rows, cols, square):
@@ -250,11 +251,16 @@ def run(s):
     return torch.nn.functional.pad(torch.cat(parts), (0, 0, 0, x.shape[0] - sum(sizes))).to(dt)
 
 
+def _powers(lo, hi):
+    """2^lo to 2^hi in 64 bits (a pow on the GPU is not exact)."""
+    return torch.tensor([math.ldexp(1.0, e) for e in range(lo, hi + 1)], dtype=torch.float64, device="cuda")
+
+
 def _exact8(v, square):
     """The values that the 8-bit form of fp64 (rows, cols) stands for, and the
     exponents, block by block of columns, by searching the bounds."""
-    exps = torch.arange(-126, 121, device=v.device)
-    bounds = torch.ldexp(torch.full((len(exps),), 448.0, dtype=torch.float64, device=v.device), exps)
+    scales, steps = _powers(-126, 121), _powers(-9, 5)
+    bounds = 448.0 * scales
     out, kept = torch.empty_like(v), []
     for c in range(0, v.shape[1], BLOCK):
         part = v[:, c:c + BLOCK]
@@ -265,22 +271,21 @@ def _exact8(v, square):
             top = whole.view(-1, BLOCK).amax(dim=1)
         at = torch.searchsorted(bounds, top)
         kept.append(at + 1)
-        e = exps[at].repeat_interleave(BLOCK)[:v.shape[0]] if square else exps[at]
-        u = torch.ldexp(part, -e[:, None])
+        scale = scales[at].repeat_interleave(BLOCK)[:v.shape[0], None] if square else scales[at][:, None]
+        u = part / scale
         # e4m3's spacing: 2^-9 under 2^-6, else an eighth of the power below
-        step = torch.exp2(torch.floor(torch.log2(u.abs().clamp(min=2.0 ** -6))) - 3)
-        out[:, c:c + BLOCK] = torch.ldexp(torch.round(u / step) * step, e[:, None])
+        step = steps[torch.frexp(u.abs().clamp(min=2.0 ** -6))[1].long() - 4 + 9]
+        out[:, c:c + BLOCK] = torch.round(u / step) * step * scale
     return out, torch.stack(kept, dim=1)
 
 
 def _double(held, square):
     q, b = held
-    e = b.to(torch.int32) - 127
-    cols = torch.arange(q.shape[-1], device=q.device) // BLOCK
-    e = e[..., cols]
+    scale = _powers(-127, 127)[b.long()]
+    scale = scale[..., torch.arange(q.shape[-1], device=q.device) // BLOCK]
     if square:
-        e = e[..., torch.arange(q.shape[-2], device=q.device) // BLOCK, :]
-    return torch.ldexp(q.double(), e)
+        scale = scale[..., torch.arange(q.shape[-2], device=q.device) // BLOCK, :]
+    return q.double() * scale
 
 
 def exact(case, seed):
