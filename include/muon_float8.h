@@ -1,0 +1,111 @@
+/*
+ * muon_float8.h - C ABI of libmuon's 8-bit floating-point layer: rows and
+ * weights in e4m3 with a power-of-two scale for each block of 128, the product
+ * of the two, the two gradient products that lead to a Muon step, and the same
+ * three grouped by expert with ragged sizes.
+ *
+ *   muon_f8_quantize      rows (a scale per 128 values) or weights (a scale
+ *                         per 128 x 128 values) to 8 bits
+ *   muon_f8_dequantize    and back
+ *   muon_f8_matmul        Y  = x w^T
+ *   muon_f8_grad_input    dX = dY w
+ *   muon_f8_grad_weight   dW = dY^T x
+ *
+ * The 8-bit form of a block v: scale = 2^e with the smallest e >= -126 for
+ * which max|v| <= 448 * 2^e, q = v / scale rounded to e4m3 (4 bits of
+ * significand, subnormals under 2^-6; nearest, ties to even).  Scales are held
+ * as e + 127 in a byte (e8m0), 255 for NaN.  A block that holds a NaN or an
+ * infinity gets scale NaN and q NaN: what is computed from it is NaN.  Products
+ * accept any e4m3 values and any such scales.
+ *
+ * Conventions:
+ *   - Matrices are row-major with unit column stride; ld* is the distance of
+ *     rows in elements (ld >= columns; ignored for at most one row).
+ *   - Rows of 8-bit values start at multiples of 16 bytes (address and ld), and
+ *     may be read up to the next multiple of 16 behind their last column, the
+ *     last row too; what stands there is irrelevant.  Other operands need no
+ *     alignment beyond the element's own.
+ *   - Scales are contiguous: of rows, ceil(cols / 128) per row; of weights,
+ *     ceil(rows / 128) such rows per matrix.
+ *   - x, y, dx, dw are fp32 or bf16 (muon_dtype); dy is bf16.
+ *   - Grouped by expert: `ends` is a device array of `experts` int32, not
+ *     falling: rows ends[e - 1] (0 for the first) to ends[e] - 1 of x, dy, y and
+ *     dx belong to expert e, whose weights stand w_stride elements behind
+ *     those of the one before.  Experts without rows are allowed; rows from
+ *     the last end on belong to none: they are not read, and are set to zero in
+ *     y and dx.  Values outside [0, t] count as the nearest of the two, and an
+ *     end before its expert's start as no rows; no memory outside the operands
+ *     is touched whatever `ends` holds.  ends NULL: all rows belong to the one
+ *     matrix (experts must be 1).
+ *   - All pointers are device pointers owned by the caller.  A call with no
+ *     output elements enqueues nothing and may be given null pointers.
+ *   - Calls enqueue on `stream`, do not synchronise and allocate nothing; they
+ *     may be captured into a graph.  A workspace's size comes from
+ *     muon_f8_workspace, its address must be 256-byte aligned, its contents
+ *     between calls are irrelevant.  Results do not depend on timing.
+ *   - Outputs may not overlap inputs.
+ *   - Errors as in muon.h: host validation first, nothing enqueued on any
+ *     status other than MUON_OK and MUON_ERR_HIP.  Dimensions above 2^24 and
+ *     more than 1024 experts give MUON_ERR_UNSUPPORTED.
+ */
+#ifndef MUON_FLOAT8_H
+#define MUON_FLOAT8_H
+
+#include "muon.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* The 8-bit form of `count` matrices, x_stride and q_stride elements apart.
+ * block_rows 1: a scale per 128 values of a row; 128: per 128 x 128 values.
+ * Each row of q is written up to its last column only. */
+muon_status muon_f8_quantize(const void* x, int64_t ldx, int64_t x_stride, muon_dtype dtype, int64_t count,
+                             int64_t rows, int64_t cols, int block_rows, uint8_t* q, int64_t ldq,
+                             int64_t q_stride, uint8_t* scale, hipStream_t stream);
+/* x = q * scale rounded to the type (exact in both within its range). */
+muon_status muon_f8_dequantize(const uint8_t* q, int64_t ldq, int64_t q_stride, const uint8_t* scale,
+                               int64_t count, int64_t rows, int64_t cols, int block_rows, void* x, int64_t ldx,
+                               int64_t x_stride, muon_dtype dtype, hipStream_t stream);
+
+/* The products below: t rows, weights n x k (out x in), one matrix per expert.
+ *   MUON_F8_MATMUL       a = xq (t x k)
+ *   MUON_F8_GRAD_INPUT   a = dy (t x n)
+ *   MUON_F8_GRAD_WEIGHT  a = dy (t x n)
+ * The workspace depends on the sizes, the type, the number of experts
+ * (grouped: ends given) and a's row distance and 16-byte alignment (addresses
+ * are not read). */
+typedef enum { MUON_F8_MATMUL = 0, MUON_F8_GRAD_INPUT = 1, MUON_F8_GRAD_WEIGHT = 2 } muon_f8_product;
+muon_status muon_f8_workspace(muon_f8_product product, const void* a, int64_t lda, int grouped, int64_t experts,
+                              int64_t t, int64_t n, int64_t k, muon_dtype dtype, size_t* workspace_bytes);
+
+/* y[t][n] = sum_k (xq[t][k] * x_scale) * (wq[n][k] * w_scale).  An fp32 result,
+ * and one of few rows, is summed in fp32 of exact products.  A bf16 result may
+ * be summed by the 8-bit matrix cores, which take eight products at a time and
+ * cut each below 2^-13 of the power of two under the largest: an error of at
+ * most 2^-10 of the sum of the products' magnitudes, 2^-16 of the result's root
+ * mean square for normally distributed operands. */
+muon_status muon_f8_matmul(const uint8_t* xq, int64_t ldx, const uint8_t* x_scale, const uint8_t* wq, int64_t ldw,
+                           int64_t w_stride, const uint8_t* w_scale, const int32_t* ends, int64_t experts, int64_t t,
+                           int64_t n, int64_t k, void* y, int64_t ldy, muon_dtype dtype, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/* dx[t][k] = sum_n dy[t][n] * (wq[n][k] * w_scale), fp32 sums. */
+muon_status muon_f8_grad_input(const void* dy, int64_t lddy, const uint8_t* wq, int64_t ldw, int64_t w_stride,
+                               const uint8_t* w_scale, const int32_t* ends, int64_t experts, int64_t t, int64_t n,
+                               int64_t k, void* dx, int64_t lddx, muon_dtype dtype, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/* dw[n][k] = sum_t dy[t][n] * (xq[t][k] * x_scale) over an expert's rows, fp32
+ * sums, one matrix per expert, dw_stride elements apart (zero without rows);
+ * accumulate != 0 adds to what dw holds (in fp32, rounded to the type). */
+muon_status muon_f8_grad_weight(const void* dy, int64_t lddy, const uint8_t* xq, int64_t ldx, const uint8_t* x_scale,
+                                const int32_t* ends, int64_t experts, int64_t t, int64_t n, int64_t k, void* dw,
+                                int64_t lddw, int64_t dw_stride, muon_dtype dtype, int accumulate, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MUON_FLOAT8_H */

@@ -1,0 +1,252 @@
+// C ABI of the 8-bit floating-point layer (include/muon_float8.h): validation,
+// the choice of kernel, tile and split, and the launch sequence.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <iterator>
+
+#include "float8.h"
+#include "linear8.h"
+#include "muon_float8.h"
+
+using namespace muon::f8;
+
+namespace {
+
+constexpr int64_t kMaxDim = 1ll << 24;
+
+bool known(muon_dtype t) { return t == MUON_F32 || t == MUON_BF16; }
+int64_t size_of(muon_dtype t) { return t == MUON_BF16 ? 2 : 4; }
+bool aligned(const void* p, int64_t a) { return (uintptr_t)p % (uintptr_t)a == 0; }
+int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+int64_t blocks_of(int64_t v) { return (v + kBlock - 1) / kBlock; }
+muon_status hip(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_ERR_HIP; }
+
+// A matrix argument: present, aligned to its elements, rows that do not
+// overlap.
+bool matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t size) {
+  return p && aligned(p, size) && (rows <= 1 || ld >= cols);
+}
+// 8-bit rows: each starts at a multiple of 16 bytes.
+bool matrix8(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+  return p && aligned(p, 16) && (rows <= 1 || (ld >= cols && ld % 16 == 0));
+}
+
+// Row tiles of `rows` that t rows need at most, however they fall on the
+// experts, and one for rows of none.
+int64_t few_slots(int64_t t, int64_t rows, int64_t experts) {
+  return experts > 0 ? t / rows + std::min(experts, t) + 1 : (t + rows - 1) / rows;
+}
+
+// How a product runs.  few: rows of the few rows' kernel, or 0.
+struct Choice {
+  Kind kind = FWD;
+  int few = 0;
+  bool pack = false;          // a laid out again
+  int64_t lda = 0, bytes = 0; // bytes of a's row as the kernel reads it; of the workspace
+  int64_t at_part = 0;
+  int tile = 128, groups = 1, splits = 1, direct = 0;
+  int np = 0, nq = 0, kd = 0;
+};
+
+Choice choose(muon_f8_product product, const void* a, int64_t lda, bool grouped, int64_t experts, int64_t t, int64_t n,
+              int64_t k, bool bf16) {
+  Choice c;
+  const bool fwd = product == MUON_F8_MATMUL, dw = product == MUON_F8_GRAD_WEIGHT;
+  c.kind = fwd ? (bf16 ? FWD : FWD32) : dw ? DW : DX;
+  c.np = (int)(fwd ? n : k);
+  c.nq = (int)(dw ? n : t);
+  c.kd = (int)(fwd ? k : dw ? t : n);
+  const int64_t a_cols = fwd ? k : n, size = fwd ? 1 : 2;
+  c.lda = t <= 1 ? up(a_cols * size, 16) : lda * size;
+  if (!fwd && t * n > 0) {
+    // bf16 rows that the DMA cannot read: not at 16 bytes, or with a last
+    // chunk that would leave the matrix
+    c.pack = !aligned(a, 16) || c.lda % 16 || a_cols % 8;
+    if (c.pack) {
+      c.lda = up(a_cols * 2, 16);
+      c.bytes = up(t * c.lda, 256);
+    }
+  }
+  const int64_t each = grouped ? (t + experts - 1) / experts : t;  // rows of x at a time
+  if (fwd && each <= 32) {
+    c.few = each <= 16 ? 16 : 32;
+    // (a launch has fewer than 2^32 threads)
+    if (up(n, 16) / 16 * few_slots(t, c.few, grouped ? experts : 0) <= (1ll << 32) / 512 - 1) return c;
+    c.few = 0;
+  }
+  auto tiles = [&](int64_t T) { return (int64_t)((c.np + T - 1) / T) * ((c.nq + T - 1) / T); };
+  c.tile = 128;
+  c.direct = (int)tiles(c.tile);
+  return c;
+}
+
+muon_status product_sizes(muon_f8_product product, bool grouped, int64_t experts, int64_t t, int64_t n, int64_t k) {
+  if (product < MUON_F8_MATMUL || product > MUON_F8_GRAD_WEIGHT) return MUON_ERR_INVALID_ARGUMENT;
+  if (t < 0 || n < 0 || k < 0 || experts < 1 || (!grouped && experts != 1)) return MUON_ERR_INVALID_ARGUMENT;
+  if (t > kMaxDim || n > kMaxDim || k > kMaxDim || experts > kMaxExperts) return MUON_ERR_UNSUPPORTED;
+  return MUON_OK;
+}
+
+// a: xq or dy; b: the weights, or the rows of the weight gradient.
+struct Call {
+  muon_f8_product product;
+  const void* a;
+  int64_t lda;
+  const uint8_t* a_scale;
+  const uint8_t* b;
+  int64_t ldb, b_stride;
+  const uint8_t* b_scale;
+  const int32_t* ends;
+  int64_t experts, t, n, k;
+  void* out;
+  int64_t ldo, o_stride;
+  muon_dtype dtype;
+  bool accumulate;
+  void* workspace;
+  size_t workspace_bytes;
+};
+
+muon_status run(const Call& v, hipStream_t s) {
+  const bool fwd = v.product == MUON_F8_MATMUL, dw = v.product == MUON_F8_GRAD_WEIGHT, grouped = v.ends != nullptr;
+  const muon_status bad = product_sizes(v.product, grouped, v.experts, v.t, v.n, v.k);
+  if (bad != MUON_OK) return bad;
+  if (!known(v.dtype) || !aligned(v.ends, 4)) return MUON_ERR_INVALID_ARGUMENT;
+  const int64_t t = v.t, n = v.n, k = v.k;
+  const int64_t a_cols = fwd ? k : n, b_rows = dw ? t : n;
+  const int64_t o_rows = dw ? n : t, o_cols = fwd ? n : k;
+  if (o_rows == 0 || o_cols == 0) return MUON_OK;
+  if (!matrix(v.out, v.ldo, o_rows, o_cols, size_of(v.dtype))) return MUON_ERR_INVALID_ARGUMENT;
+  if (t * a_cols > 0 && !(fwd ? matrix8(v.a, v.lda, t, a_cols) : matrix(v.a, v.lda, t, a_cols, 2)))
+    return MUON_ERR_INVALID_ARGUMENT;
+  if (b_rows * k > 0 && !matrix8(v.b, v.ldb, b_rows, k)) return MUON_ERR_INVALID_ARGUMENT;
+  if ((fwd && t * k > 0 && !v.a_scale) || (b_rows * k > 0 && !v.b_scale)) return MUON_ERR_INVALID_ARGUMENT;
+  if (v.experts > 1) {
+    // one expert's matrix behind the other's
+    if (dw && v.o_stride < (o_rows - 1) * v.ldo + o_cols) return MUON_ERR_INVALID_ARGUMENT;
+    if (!dw && n * k > 0 && (v.b_stride % 16 || v.b_stride < (n > 1 ? (n - 1) * v.ldb : 0) + k))
+      return MUON_ERR_INVALID_ARGUMENT;
+  }
+  const Choice c = choose(v.product, v.a, v.lda, grouped, v.experts, t, n, k, v.dtype == MUON_BF16);
+  if (c.bytes > 0) {
+    if (v.workspace_bytes < (size_t)c.bytes) return MUON_ERR_WORKSPACE_TOO_SMALL;
+    if (!v.workspace || !aligned(v.workspace, 256)) return MUON_ERR_INVALID_ARGUMENT;
+  }
+  char* const w = (char*)v.workspace;
+  MmParams p = {};
+  p.Q = c.pack ? w : (const char*)v.a;
+  p.P = (const char*)v.b;
+  p.sp = v.b_scale;
+  p.sq = v.a_scale;
+  p.ends = v.ends;
+  p.ldp = b_rows <= 1 ? up(k, 16) : v.ldb;
+  p.ldq = c.lda;
+  p.ldsp = (int)blocks_of(k);
+  p.ldsq = (int)blocks_of(a_cols);
+  p.stride_p = v.b_stride;
+  p.stride_sp = blocks_of(n) * blocks_of(k);
+  p.stride_o = v.o_stride;
+  p.experts = (int)v.experts;
+  p.np = c.np;
+  p.nq = c.nq;
+  p.kd = c.kd;
+  p.tile = c.tile;
+  p.groups = c.groups;
+  p.direct = c.direct;
+  p.splits = c.splits;
+  p.out = v.out;
+  p.ldo = v.ldo;
+  p.obf16 = v.dtype == MUON_BF16;
+  p.accumulate = v.accumulate;
+  p.part = c.splits > 1 ? (float*)(w + c.at_part) : nullptr;
+  if (c.few) return hip(launch_few(p, c.few, s));
+  hipError_t e = hipSuccess;
+  if (c.pack) e = muon::l8::launch_pack(v.a, t > 1 ? v.lda * 2 : 0, a_cols * 2, w, c.lda, t, s);
+  if (e == hipSuccess) e = launch_mm(p, c.kind, s);
+  return hip(e);
+}
+
+// Checks of a call that makes or reads the 8-bit form.
+muon_status form_sizes(muon_dtype dtype, int64_t count, int64_t rows, int64_t cols, int block_rows) {
+  if (!known(dtype) || count < 0 || rows < 0 || cols < 0 || (block_rows != 1 && block_rows != kBlock))
+    return MUON_ERR_INVALID_ARGUMENT;
+  if (rows > kMaxDim || cols > kMaxDim || count > kMaxDim) return MUON_ERR_UNSUPPORTED;
+  return MUON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_f8_quantize(const void* x, int64_t ldx, int64_t x_stride, muon_dtype dtype, int64_t count,
+                             int64_t rows, int64_t cols, int block_rows, uint8_t* q, int64_t ldq, int64_t q_stride,
+                             uint8_t* scale, hipStream_t stream) {
+  const muon_status bad = form_sizes(dtype, count, rows, cols, block_rows);
+  if (bad != MUON_OK) return bad;
+  if (count == 0 || rows == 0 || cols == 0) return MUON_OK;
+  if (!matrix(x, ldx, rows, cols, size_of(dtype)) || !matrix8(q, ldq, rows, cols) || !scale ||
+      (count > 1 && (q_stride % 16 || q_stride < (rows - 1) * ldq + cols)))
+    return MUON_ERR_INVALID_ARGUMENT;
+  const FormParams p = {(void*)x, q, scale, count, rows, cols, ldx, x_stride, ldq, q_stride, block_rows};
+  return hip(launch_quantize(p, dtype == MUON_BF16, stream));
+}
+
+muon_status muon_f8_dequantize(const uint8_t* q, int64_t ldq, int64_t q_stride, const uint8_t* scale, int64_t count,
+                               int64_t rows, int64_t cols, int block_rows, void* x, int64_t ldx, int64_t x_stride,
+                               muon_dtype dtype, hipStream_t stream) {
+  const muon_status bad = form_sizes(dtype, count, rows, cols, block_rows);
+  if (bad != MUON_OK) return bad;
+  if (count == 0 || rows == 0 || cols == 0) return MUON_OK;
+  if (!matrix(x, ldx, rows, cols, size_of(dtype)) || !matrix8(q, ldq, rows, cols) || !scale ||
+      (count > 1 && (q_stride % 16 || x_stride < (rows - 1) * ldx + cols)))
+    return MUON_ERR_INVALID_ARGUMENT;
+  const FormParams p = {x, (uint8_t*)q, (uint8_t*)scale, count, rows, cols, ldx, x_stride, ldq, q_stride, block_rows};
+  return hip(launch_dequantize(p, dtype == MUON_BF16, stream));
+}
+
+muon_status muon_f8_workspace(muon_f8_product product, const void* a, int64_t lda, int grouped, int64_t experts,
+                              int64_t t, int64_t n, int64_t k, muon_dtype dtype, size_t* workspace_bytes) {
+  if (!workspace_bytes || !known(dtype)) return MUON_ERR_INVALID_ARGUMENT;
+  const muon_status bad = product_sizes(product, grouped != 0, experts, t, n, k);
+  if (bad != MUON_OK) return bad;
+  *workspace_bytes = (size_t)choose(product, a, lda, grouped != 0, experts, t, n, k, dtype == MUON_BF16).bytes;
+  return MUON_OK;
+}
+
+// (float8.h)
+void muon_f8_choice(int product, const void* a, int64_t lda, int grouped, int64_t experts, int64_t t, int64_t n,
+                    int64_t k, int bf16, int64_t* out) {
+  const Choice c = choose((muon_f8_product)product, a, lda, grouped != 0, experts, t, n, k, bf16 != 0);
+  const int64_t T = c.tile, tiles = c.few ? 0 : (c.np + T - 1) / T * ((c.nq + T - 1) / T);
+  const int64_t v[] = {c.kind, c.few, T, c.groups, c.pack, c.direct, tiles - c.direct, c.splits};
+  std::copy(std::begin(v), std::end(v), out);
+}
+
+muon_status muon_f8_matmul(const uint8_t* xq, int64_t ldx, const uint8_t* x_scale, const uint8_t* wq, int64_t ldw,
+                           int64_t w_stride, const uint8_t* w_scale, const int32_t* ends, int64_t experts, int64_t t,
+                           int64_t n, int64_t k, void* y, int64_t ldy, muon_dtype dtype, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  return run({MUON_F8_MATMUL, xq, ldx, x_scale, wq, ldw, w_stride, w_scale, ends, experts, t, n, k, y, ldy, 0, dtype,
+              false, workspace, workspace_bytes},
+             stream);
+}
+
+muon_status muon_f8_grad_input(const void* dy, int64_t lddy, const uint8_t* wq, int64_t ldw, int64_t w_stride,
+                               const uint8_t* w_scale, const int32_t* ends, int64_t experts, int64_t t, int64_t n,
+                               int64_t k, void* dx, int64_t lddx, muon_dtype dtype, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
+  return run({MUON_F8_GRAD_INPUT, dy, lddy, nullptr, wq, ldw, w_stride, w_scale, ends, experts, t, n, k, dx, lddx, 0,
+              dtype, false, workspace, workspace_bytes},
+             stream);
+}
+
+muon_status muon_f8_grad_weight(const void* dy, int64_t lddy, const uint8_t* xq, int64_t ldx, const uint8_t* x_scale,
+                                const int32_t* ends, int64_t experts, int64_t t, int64_t n, int64_t k, void* dw,
+                                int64_t lddw, int64_t dw_stride, muon_dtype dtype, int accumulate, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  return run({MUON_F8_GRAD_WEIGHT, dy, lddy, nullptr, xq, ldx, 0, x_scale, ends, experts, t, n, k, dw, lddw, dw_stride,
+              dtype, accumulate != 0, workspace, workspace_bytes},
+             stream);
+}
+
+}  // extern "C"

@@ -40,8 +40,16 @@ class MuonMI355X:
                 raise ValueError("gradient shape/dtype/layout does not match the plan")
 
     def step(self, grads: Sequence[torch.Tensor], lr: float, weight_decay: float,
-             refresh: Optional[bool] = None, out: Optional[List[torch.Tensor]] = None):
+             refresh: Optional[bool] = None, out: Optional[List[torch.Tensor]] = None,
+             max_norm: Optional[float] = None):
+        """One step.  With max_norm, the gradients are first scaled in place to a
+        global norm of at most that (clip.clip_grad_norm), and the norm they
+        had is returned."""
         self._check(grads)
+        norm = None
+        if max_norm is not None:
+            from .clip import clip_grad_norm
+            norm = clip_grad_norm(grads, max_norm)
         if refresh is None:
             refresh = self.refresh_period <= 0 or self.t % self.refresh_period == 0
         stream = torch.cuda.current_stream(self.params[0].device).cuda_stream
@@ -54,3 +62,4 @@ class MuonMI355X:
         else:
             self.plan.rownorm_ptrs(*args)
         self.t += 1
+        return norm
