@@ -8,8 +8,8 @@
 namespace muon {
 namespace clip {
 
-// A tensor of a launch.  Its elements are taken `chunk` at a time, a workgroup
-// each, the first of which is the launch's workgroup `first`.
+// A tensor of a launch: a workgroup for each `chunk` of its elements, the first
+// of which is the launch's workgroup `first`.
 struct Tensor {
   const void* g;
   void* out;
@@ -27,7 +27,7 @@ struct Table {
 };
 static_assert(sizeof(Table) + 64 <= 4096, "kernel arguments");
 
-// part[from + workgroup] = the sum of a chunk's squares.
+// part[from + workgroup] = the sum of its squares.
 hipError_t launch_squares(const Table& t, double* part, int64_t from, hipStream_t s);
 // norm[0] from `count` partial sums (one workgroup).
 hipError_t launch_norm(const double* part, int64_t count, float* norm, hipStream_t s);

@@ -7,9 +7,9 @@
 // workgroups: the same bits on every run.
 //
 // Bound by HBM: a square costs a conversion and a 64-bit fma, a fraction of its
-// load.  The second pass takes the chunks in the opposite order, so that what
-// the first read last comes from the last-level cache; where nothing is clipped
-// in place it reads no gradient at all.
+// load.  The second pass goes through the tensors backwards, so that what the
+// first read last comes from the last-level cache; where nothing is clipped in
+// place it reads no gradient at all.
 #include "clip.h"
 #include "common.hpp"
 
@@ -52,41 +52,50 @@ __device__ __forceinline__ int find(const Table& t, uint32_t b) {
   return lo;
 }
 
-// Calls f(place, elements, n) for the run's 16-byte pieces, U of a thread's in
-// flight, and for the elements left over.  `elements` holds n of them.
-template <typename E, typename F>
-__device__ __forceinline__ void each(const E* g, int64_t n, F f) {
-  constexpr int PV = 16 / sizeof(E), U = 4;
-  int64_t i = (int64_t)threadIdx.x * PV;
-  for (; i + (int64_t)(U - 1) * NT * PV + PV <= n; i += (int64_t)U * NT * PV) {
+// Calls f(place, elements, n) for what workgroup j of `groups` takes of n
+// elements: every groups-th piece of U 16-byte loads per thread (all workgroups
+// sweep the tensor side by side: streams of their own, a chunk apart, reached
+// 4.8 TB/s), from the last to the first if BACK; and one of them what is left
+// over.  `elements` holds n of them, zeros behind.
+template <bool BACK, typename E, typename F>
+__device__ __forceinline__ void each(const E* g, int64_t n, uint32_t j, uint32_t groups, F f) {
+  constexpr int PV = 16 / sizeof(E), U = 4, PIECE = NT * PV * U;
+  const int64_t pieces = n / PIECE;
+  const int64_t mine = pieces > j ? (pieces - j + groups - 1) / groups : 0;
+  for (int64_t k = 0; k < mine; ++k) {
+    const int64_t i = (j + (BACK ? mine - 1 - k : k) * groups) * PIECE + (int64_t)threadIdx.x * PV;
     V v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = *(const V*)(g + i + (int64_t)u * NT * PV);
+    for (int u = 0; u < U; ++u) {
+      if constexpr (BACK) v[u] = __builtin_nontemporal_load((const V*)(g + i + u * NT * PV));
+      else v[u] = *(const V*)(g + i + u * NT * PV);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       E e[PV];
       __builtin_memcpy(e, &v[u], 16);
-      f(i + (int64_t)u * NT * PV, e, PV);
+      f(i + u * NT * PV, e, PV);
     }
   }
-  for (; i < n; i += (int64_t)NT * PV) {
+  if (j != pieces % groups) return;
+  for (int64_t i = pieces * PIECE + (int64_t)threadIdx.x * PV; i < n; i += NT * PV) {
     E e[PV];
     const int m = (int)(n - i < PV ? n - i : PV);
     if (m == PV) {
       __builtin_memcpy(e, g + i, 16);
     } else {
 #pragma unroll
-      for (int j = 0; j < PV; ++j) e[j] = j < m ? g[i + j] : (E)0;
+      for (int l = 0; l < PV; ++l) e[l] = l < m ? g[i + l] : (E)0;
     }
     f(i, e, m);
   }
 }
 
 template <typename E>
-__device__ __forceinline__ double squares(const E* g, int64_t n) {
+__device__ __forceinline__ double squares(const E* g, int64_t n, uint32_t j, uint32_t groups) {
   constexpr int PV = 16 / sizeof(E);
   double sum[4] = {0.0, 0.0, 0.0, 0.0};
-  each(g, n, [&](int64_t, const E* e, int) {  // (zeros behind the last)
+  each<false>(g, n, j, groups, [&](int64_t, const E* e, int) {
 #pragma unroll
     for (int j = 0; j < PV; ++j) {
       const double d = (double)wide<E>(e[j]);
@@ -98,8 +107,8 @@ __device__ __forceinline__ double squares(const E* g, int64_t n) {
 
 __global__ void __launch_bounds__(NT) squares_kernel(const Table t, double* part) {
   const Tensor& x = t.t[find(t, blockIdx.x)];
-  const int64_t at = (int64_t)(blockIdx.x - x.first) * t.chunk, n = x.n - at < t.chunk ? x.n - at : t.chunk;
-  double v = x.gbf16 ? squares((const uint16_t*)x.g + at, n) : squares((const float*)x.g + at, n);
+  const uint32_t j = blockIdx.x - x.first, groups = (uint32_t)((x.n + t.chunk - 1) / t.chunk);
+  double v = x.gbf16 ? squares((const uint16_t*)x.g, x.n, j, groups) : squares((const float*)x.g, x.n, j, groups);
   v = group_sum(v);
   if (threadIdx.x == 0) part[blockIdx.x] = v;
 }
@@ -118,14 +127,20 @@ __global__ void __launch_bounds__(NT) norm_kernel(const double* part, int64_t co
 }
 
 template <typename E, typename O>
-__device__ __forceinline__ void scale(const E* g, O* out, int64_t n, float by) {
+__device__ __forceinline__ void scale(const E* g, O* out, int64_t n, uint32_t j, uint32_t groups, float by) {
   constexpr int PV = 16 / sizeof(E);
-  each(g, n, [&](int64_t i, const E* e, int m) {
+  each<true>(g, n, j, groups, [&](int64_t i, const E* e, int m) {
     O o[PV];
 #pragma unroll
-    for (int j = 0; j < PV; ++j) o[j] = narrow<O>(wide<E>(e[j]) * by);
+    for (int l = 0; l < PV; ++l) o[l] = narrow<O>(wide<E>(e[l]) * by);
     if (m == PV) {
-      __builtin_memcpy(out + i, o, sizeof(o));
+      // (past the caches, which hold what the first pass read last)
+      constexpr int WB = sizeof(O) * PV < 16 ? 8 : 16, NW = sizeof(O) * PV / WB;
+      typedef uint32_t W __attribute__((ext_vector_type(WB / 4), aligned(2)));
+      W w[NW];
+      __builtin_memcpy(w, o, NW * WB);
+#pragma unroll
+      for (int j = 0; j < NW; ++j) __builtin_nontemporal_store(w[j], (W*)(out + i) + j);
     } else {
 #pragma unroll
       for (int j = 0; j < PV; ++j)
@@ -143,15 +158,15 @@ __global__ void __launch_bounds__(NT) scale_kernel(const Table t, const double* 
   const float by = kept ? 1.0f : (float)((double)max_norm / v);
   const Tensor& x = t.t[find(t, b)];
   if (kept && x.g == x.out) return;
-  const int64_t at = (int64_t)(b - x.first) * t.chunk, n = x.n - at < t.chunk ? x.n - at : t.chunk;
+  const uint32_t j = b - x.first, groups = (uint32_t)((x.n + t.chunk - 1) / t.chunk);
   if (x.gbf16) {
-    const uint16_t* g = (const uint16_t*)x.g + at;
-    if (x.obf16) scale(g, (uint16_t*)x.out + at, n, by);
-    else scale(g, (float*)x.out + at, n, by);
+    const uint16_t* g = (const uint16_t*)x.g;
+    if (x.obf16) scale(g, (uint16_t*)x.out, x.n, j, groups, by);
+    else scale(g, (float*)x.out, x.n, j, groups, by);
   } else {
-    const float* g = (const float*)x.g + at;
-    if (x.obf16) scale(g, (uint16_t*)x.out + at, n, by);
-    else scale(g, (float*)x.out + at, n, by);
+    const float* g = (const float*)x.g;
+    if (x.obf16) scale(g, (uint16_t*)x.out, x.n, j, groups, by);
+    else scale(g, (float*)x.out, x.n, j, groups, by);
   }
 }
 

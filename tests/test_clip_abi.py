@@ -76,8 +76,8 @@ def test_workspaces(n):
     _, b, c = arrays((P,) * len(n), n, (0,) * len(n))
     z = ctypes.c_size_t()
     assert abi().muon_clip_workspace(len(n), b, c, ctypes.addressof(z)) == OK
-    # a partial sum for each chunk: the chunks of one launch run at once
-    assert z.value % 8 == 0 and sum(v > 0 for v in n) <= z.value // 8 <= 2048 + len(n)
+    # a partial sum for each workgroup
+    assert z.value % 8 == 0 and sum(v > 0 for v in n) <= z.value // 8 <= 4096 + len(n)
     assert abi().muon_clip_workspace(len(n), b, c, None) == INVALID
 
 
