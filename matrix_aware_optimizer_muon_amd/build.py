@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmuon.so")
 SOURCES = ["gemm.hip", "gemm_dma.hip", "rr_fused.hip", "direct_fused.hip", "elementwise.hip", "muon_api.cpp",
-           "linear8_rows.hip", "linear8_gemm.hip", "linear8_api.cpp", "float8_rows.hip", "float8_gemm.hip",
+           "linear8_rows.hip", "linear8_gemm.hip", "linear8_api.cpp", "float8_rows.hip", "float8_forward.hip", "float8_grads.hip",
            "float8_api.cpp", "clip.hip", "clip_api.cpp"]
 BINDINGS = {"_linear8.so": "linear8_torch.cpp", "_float8.so": "float8_torch.cpp", "_clip.so": "clip_torch.cpp"}
 ARCH = os.environ.get("MUON_OFFLOAD_ARCH", "gfx950")

@@ -1,6 +1,6 @@
 // Internal launch interface of the 8-bit floating-point layer's kernels
 // (include/muon_float8.h): float8_rows.hip holds the 8-bit form and back,
-// float8_gemm.hip the products, float8_api.cpp validates and dispatches.
+// float8_forward.hip and float8_grads.hip the products, float8_api.cpp validates and dispatches.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -57,10 +57,17 @@ struct MmParams {
   bool obf16, accumulate;
   float* part;              // [split tiles][splits][tile][tile]
 };
-hipError_t launch_mm(const MmParams& p, Kind kind, hipStream_t s);
+hipError_t launch_forward(const MmParams& p, Kind kind, hipStream_t s);
+hipError_t launch_grads(const MmParams& p, Kind kind, hipStream_t s);
+// The split tiles' partial sums added (called by the two).
+hipError_t launch_sums(const MmParams& p, hipStream_t s);
 
-// The forward product for few rows of x (of each expert): `rows` (16, 32 or
-// 64) at a time against 16 rows of w, which is read straight from memory.
+// Row tiles of T that t rows need at most, however they fall on the experts (a
+// partly filled one each), and one for rows of no expert.
+inline int64_t row_tiles(int64_t t, int64_t T, int64_t experts) { return t / T + (experts < t ? experts : t) + 1; }
+
+// The forward product for few rows of x (of each expert): `rows` (16 or 32) at
+// a time against 16 rows of w, which is read straight from memory.
 hipError_t launch_few(const MmParams& p, int rows, hipStream_t s);
 
 }  // namespace f8

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <iterator>
 
 #include "float8.h"
@@ -27,15 +28,11 @@ muon_status hip(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_ERR_HIP;
 bool matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t size) {
   return p && aligned(p, size) && (rows <= 1 || ld >= cols);
 }
-// 8-bit rows: each starts at a multiple of 16 bytes.
+// 8-bit rows: each starts at a multiple of 16 bytes.  (Kernels add up a tile's
+// row distances in 32 bits: kMaxLd.)
+constexpr int64_t kMaxLd = 1ll << 24;
 bool matrix8(const void* p, int64_t ld, int64_t rows, int64_t cols) {
   return p && aligned(p, 16) && (rows <= 1 || (ld >= cols && ld % 16 == 0));
-}
-
-// Row tiles of `rows` that t rows need at most, however they fall on the
-// experts, and one for rows of none.
-int64_t few_slots(int64_t t, int64_t rows, int64_t experts) {
-  return experts > 0 ? t / rows + std::min(experts, t) + 1 : (t + rows - 1) / rows;
 }
 
 // How a product runs.  few: rows of the few rows' kernel, or 0.
@@ -48,6 +45,111 @@ struct Choice {
   int tile = 128, groups = 1, splits = 1, direct = 0;
   int np = 0, nq = 0, kd = 0;
 };
+
+// Measured times of a tile, us: per stage of its sum (128 bytes of K forward, 32
+// rows or columns of the gradients), and what is ahead of and behind it, for
+// workgroups that run at once: a tile of 256 or a 128-wide one of two wave groups
+// per compute unit, two 128-wide ones of one group, one 64-wide of four.
+struct Cost {
+  double stage, ends;
+};
+struct Costs {
+  Cost t256, t128, t128g2, t64g4;
+};
+const Costs kCosts[] = {
+    {{1.37, 10.5}, {0.89, 6.0}, {1.00, 4.9}, {1.05, 4.2}},  // FWD
+    {{0.0, 0.0}, {1.58, 6.9}, {1.60, 6.3}, {1.35, 4.5}},    // FWD32 (no 256-wide tile)
+    {{0.78, 8.7}, {0.52, 6.1}, {0.535, 6.0}, {0.69, 2.8}},  // DX
+    {{0.79, 8.3}, {0.54, 6.2}, {0.545, 6.1}, {0.70, 2.8}},  // DW
+};
+
+// The few rows' kernel, us: the read of w and, growing with the rows, of x; a
+// wave's chain of loads where there are few workgroups.
+double few_us(double matrices, double rows, int few, int64_t n, int64_t k) {
+  const double read = matrices * (double)n * (double)k * (few == 16 ? 1.0 : 1.2) / 6.2e6;
+  const double chain = (double)((k + 1023) / 1024) * 0.53;
+  return 2.8 + std::max(read, chain) * (1.0 + 0.033 * (rows - 1.0));
+}
+
+// The cheapest way for one matrix: workgroups take a tile each in whole rounds;
+// the tiles left over may be split along K over one more round, for a second
+// launch (4 us) and their partial sums' way to memory and back (at 4 TB/s).
+void choose_dense(Choice& c) {
+  const Costs& costs = kCosts[c.kind];
+  const bool fwd = c.kind == FWD || c.kind == FWD32;
+  const int64_t stages = fwd ? blocks_of(c.kd) : (c.kd + 31) / 32;
+  auto tiles = [&](int64_t T) { return (int64_t)((c.np + T - 1) / T) * ((c.nq + T - 1) / T); };
+  double best = 0.0;
+  auto way = [&](int tile, int groups, const Cost& cost) {
+    const int64_t all = tiles(tile), slots = tile == 128 && groups == 1 ? 512 : 256, rest = all % slots;
+    const int64_t each = (stages + groups - 1) / groups;  // a group's stages
+    const double whole = (double)(all / slots) * (cost.stage * (double)each + cost.ends);
+    double us = whole + (rest > 0 ? cost.stage * (double)each + cost.ends : 0.0);
+    int splits = 1;
+    const int64_t most = rest > 0 ? std::min<int64_t>({slots / rest, each / (fwd ? 2 : 4), 32}) : 1;
+    for (int64_t n = 2; n <= most; ++n) {
+      const double with = whole + cost.stage * (double)((each + n - 1) / n) + cost.ends + 4.0 +
+                          (double)tile * tile * 8 / 4e6 * (double)(rest * n);
+      if (with < us) {
+        us = with;
+        splits = (int)n;
+      }
+    }
+    if (best == 0.0 || us < best) {
+      best = us;
+      c.tile = tile;
+      c.groups = groups;
+      c.splits = splits;
+      c.direct = (int)(splits > 1 ? all - rest : all);
+    }
+  };
+  // (wave groups that share K need a compute unit of their own)
+  if (tiles(128) <= 256) way(128, 2, costs.t128g2);
+  else way(128, 1, costs.t128);
+  if (costs.t256.stage > 0) way(256, 1, costs.t256);
+  if (tiles(64) <= 256) way(64, 4, costs.t64g4);
+  if (fwd)
+    for (const int few : {16, 32})
+      if (c.nq <= few && few_us(1.0, (double)c.nq, few, c.np, c.kd) < best) {
+        c.few = few;
+        break;
+      }
+}
+
+// The same for experts, whose rows only the device knows: their number of tiles
+// is taken as if they shared the rows evenly, with half a tile more each.  No
+// splits: the tiles of many experts fill the card.
+void choose_experts(Choice& c, int64_t experts, int64_t t) {
+  const Costs& costs = kCosts[c.kind];
+  const bool fwd = c.kind == FWD || c.kind == FWD32;
+  const double busy = (double)std::min(experts, t), rows = (double)t / std::max(busy, 1.0);
+  auto rounds = [](double tiles, double slots) { return std::max(1.0, tiles / slots); };
+  auto columns = [&](int64_t T, int64_t n) { return (double)((n + T - 1) / T); };
+  auto way = [&](int64_t T, const Cost& cost, double slots) {
+    if (c.kind == DW) {
+      // the tiles' number is known, their sums are not: with less than two rounds
+      // the longest expert's counts (taken as twice the mean)
+      const double tiles = (double)experts * columns(T, c.np) * columns(T, c.nq);
+      return rounds(tiles, slots) * (cost.stage * rows / 32.0 + cost.ends) + (tiles < 2 * slots ? cost.stage * rows / 32.0 : 0.0);
+    }
+    const double stages = fwd ? (double)blocks_of(c.kd) : (double)((c.kd + 31) / 32);
+    const double tiles = busy * std::max(1.0, rows / (double)T + 0.5) * columns(T, c.np);
+    // (alone on its compute unit a 128-wide tile has a stage in two thirds of the time)
+    const double stage = T == 128 && tiles <= 256 ? cost.stage * 0.67 : cost.stage;
+    return std::ceil(rounds(tiles, slots)) * (stage * stages + cost.ends);
+  };
+  double best = way(128, costs.t128, 512);
+  c.tile = 128;
+  if (costs.t256.stage > 0) {
+    const double us = way(256, costs.t256, 256);
+    if (us < best) {
+      best = us;
+      c.tile = 256;
+    }
+  }
+  // (an expert's rows vary: up to a mean of half the kernel's)
+  if (fwd && rows <= 8.0 && few_us(busy, 4.0 * rows - 3.0, 16, c.np, c.kd) < best) c.few = 16;
+}
 
 Choice choose(muon_f8_product product, const void* a, int64_t lda, bool grouped, int64_t experts, int64_t t, int64_t n,
               int64_t k, bool bf16) {
@@ -68,16 +170,15 @@ Choice choose(muon_f8_product product, const void* a, int64_t lda, bool grouped,
       c.bytes = up(t * c.lda, 256);
     }
   }
-  const int64_t each = grouped ? (t + experts - 1) / experts : t;  // rows of x at a time
-  if (fwd && each <= 32) {
-    c.few = each <= 16 ? 16 : 32;
-    // (a launch has fewer than 2^32 threads)
-    if (up(n, 16) / 16 * few_slots(t, c.few, grouped ? experts : 0) <= (1ll << 32) / 512 - 1) return c;
-    c.few = 0;
+  if (grouped) choose_experts(c, experts, t);
+  else choose_dense(c);
+  // (a launch has fewer than 2^32 threads)
+  if (c.few && up(n, 16) / 16 * (grouped ? row_tiles(t, c.few, experts) : 1) > (1ll << 32) / 512 - 1) c.few = 0;
+  if (c.splits > 1) {
+    c.at_part = c.bytes;
+    const int64_t T = c.tile;
+    c.bytes += ((c.np + T - 1) / T * ((c.nq + T - 1) / T) - c.direct) * c.splits * T * T * 4;
   }
-  auto tiles = [&](int64_t T) { return (int64_t)((c.np + T - 1) / T) * ((c.nq + T - 1) / T); };
-  c.tile = 128;
-  c.direct = (int)tiles(c.tile);
   return c;
 }
 
@@ -117,6 +218,7 @@ muon_status run(const Call& v, hipStream_t s) {
   const int64_t o_rows = dw ? n : t, o_cols = fwd ? n : k;
   if (o_rows == 0 || o_cols == 0) return MUON_OK;
   if (!matrix(v.out, v.ldo, o_rows, o_cols, size_of(v.dtype))) return MUON_ERR_INVALID_ARGUMENT;
+  if ((fwd && t > 1 && v.lda > kMaxLd) || (b_rows > 1 && v.ldb > kMaxLd)) return MUON_ERR_UNSUPPORTED;
   if (t * a_cols > 0 && !(fwd ? matrix8(v.a, v.lda, t, a_cols) : matrix(v.a, v.lda, t, a_cols, 2)))
     return MUON_ERR_INVALID_ARGUMENT;
   if (b_rows * k > 0 && !matrix8(v.b, v.ldb, b_rows, k)) return MUON_ERR_INVALID_ARGUMENT;
@@ -162,7 +264,7 @@ muon_status run(const Call& v, hipStream_t s) {
   if (c.few) return hip(launch_few(p, c.few, s));
   hipError_t e = hipSuccess;
   if (c.pack) e = muon::l8::launch_pack(v.a, t > 1 ? v.lda * 2 : 0, a_cols * 2, w, c.lda, t, s);
-  if (e == hipSuccess) e = launch_mm(p, c.kind, s);
+  if (e == hipSuccess) e = fwd ? launch_forward(p, c.kind, s) : launch_grads(p, c.kind, s);
   return hip(e);
 }
 
