@@ -41,8 +41,8 @@ muon_status muon_grad_norm(int num, const void* const* g, const int64_t* numel, 
 /* The norm as above, and out[i] = the clipped g[i] in out_dtypes[i]; max_norm
  * >= 0, which may be infinite (never clips).  out[i] may be g[i] itself (with its type): then
  * nothing is written unless the norm is over max_norm.  Apart from that, no
- * out may overlap a g or another out, nor, where out[i] is g[i], one g another:
- * ranges of addresses that do give MUON_ERR_INVALID_ARGUMENT. */
+ * out (nor the norm) may overlap a g or another out, nor, where out[i] is g[i],
+ * one g another: ranges of addresses that do give MUON_ERR_INVALID_ARGUMENT. */
 muon_status muon_clip_grads(int num, const void* const* g, const int64_t* numel, const muon_dtype* dtypes,
                             void* const* out, const muon_dtype* out_dtypes, float max_norm, float* norm,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);

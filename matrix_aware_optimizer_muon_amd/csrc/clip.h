@@ -27,6 +27,11 @@ struct Table {
 };
 static_assert(sizeof(Table) + 64 <= 4096, "kernel arguments");
 
+// All of it for few elements, in one launch: at most kSmallGroups workgroups'
+// shares at a chunk of kSmallChunk.
+constexpr int64_t kSmallChunk = 2048, kSmallGroups = 16;
+hipError_t launch_small(const Table& t, bool scaled, float max_norm, float* norm, hipStream_t s);
+
 // part[from + workgroup] = the sum of its squares.
 hipError_t launch_squares(const Table& t, double* part, int64_t from, hipStream_t s);
 // norm[0] from `count` partial sums (one workgroup).

@@ -28,17 +28,28 @@ template <typename E> __device__ __forceinline__ E narrow(float v);
 template <> __device__ __forceinline__ uint16_t narrow<uint16_t>(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
 
-// The sum over the workgroup, the same order each time, in every thread.
+// The sum over a workgroup of W waves, the same order each time, in every thread.
+template <int W = NT / 64>
 __device__ __forceinline__ double group_sum(double v) {
-  __shared__ double s_sum[NT / 64];
+  __shared__ double s_sum[W];
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
   if (threadIdx.x % 64 == 0) s_sum[threadIdx.x / 64] = v;
   __syncthreads();
   v = 0.0;
 #pragma unroll
-  for (int w = 0; w < NT / 64; ++w) v += s_sum[w];
+  for (int w = 0; w < W; ++w) v += s_sum[w];
   return v;
+}
+
+// The factor that takes a norm to at most max_norm.
+struct Factor {
+  bool kept;
+  float by;
+};
+__device__ __forceinline__ Factor factor(double norm, float max_norm) {
+  const bool kept = norm <= (double)max_norm;
+  return {kept, kept ? 1.0f : (float)((double)max_norm / norm)};
 }
 
 // The tensor that workgroup b belongs to.
@@ -154,24 +165,106 @@ __global__ void __launch_bounds__(NT) scale_kernel(const Table t, const double* 
   const uint32_t b = t.groups - 1 - blockIdx.x;
   const double v = norm_of(part, count);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)v;
-  const bool kept = v <= (double)max_norm;
-  const float by = kept ? 1.0f : (float)((double)max_norm / v);
+  const Factor f = factor(v, max_norm);
   const Tensor& x = t.t[find(t, b)];
-  if (kept && x.g == x.out) return;
+  if (f.kept && x.g == x.out) return;
   const uint32_t j = b - x.first, groups = (uint32_t)((x.n + t.chunk - 1) / t.chunk);
   if (x.gbf16) {
     const uint16_t* g = (const uint16_t*)x.g;
-    if (x.obf16) scale(g, (uint16_t*)x.out, x.n, j, groups, by);
-    else scale(g, (float*)x.out, x.n, j, groups, by);
+    if (x.obf16) scale(g, (uint16_t*)x.out, x.n, j, groups, f.by);
+    else scale(g, (float*)x.out, x.n, j, groups, f.by);
   } else {
     const float* g = (const float*)x.g;
-    if (x.obf16) scale(g, (uint16_t*)x.out, x.n, j, groups, by);
-    else scale(g, (float*)x.out, x.n, j, groups, by);
+    if (x.obf16) scale(g, (uint16_t*)x.out, x.n, j, groups, f.by);
+    else scale(g, (float*)x.out, x.n, j, groups, f.by);
+  }
+}
+
+// Few elements: one workgroup does all of it, a wave per kSmallChunk elements, so
+// that a call is one launch.  `scaled` says whether there is anything to write
+// but the norm.
+template <typename E, typename F>
+__device__ __forceinline__ void wave_each(const E* g, int n, F f) {
+  constexpr int PV = 16 / sizeof(E), U = kSmallChunk / (64 * PV);
+  const int lane = threadIdx.x % 64;
+  V v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = (u * 64 + lane) * PV;
+    if (i + PV <= n) v[u] = *(const V*)(g + i);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = (u * 64 + lane) * PV, m = n - i < PV ? n - i : PV;
+    E e[PV];
+    if (m == PV) {
+      __builtin_memcpy(e, &v[u], 16);
+    } else {
+#pragma unroll
+      for (int l = 0; l < PV; ++l) e[l] = l < m ? g[i + l] : (E)0;
+    }
+    if (m > 0) f(i, e, m);
+  }
+}
+template <typename E, typename O>
+__device__ __forceinline__ void wave_scale(const E* g, O* out, int n, float by) {
+  constexpr int PV = 16 / sizeof(E);
+  wave_each(g, n, [&](int i, const E* e, int m) {
+    O o[PV];
+#pragma unroll
+    for (int l = 0; l < PV; ++l) o[l] = narrow<O>(wide<E>(e[l]) * by);
+    if (m == PV) {
+      __builtin_memcpy(out + i, o, sizeof(o));
+    } else {
+#pragma unroll
+      for (int l = 0; l < PV; ++l)
+        if (l < m) out[i + l] = o[l];
+    }
+  });
+}
+constexpr int kSmallWaves = kSmallGroups;
+__global__ void __launch_bounds__(64 * kSmallWaves) small_kernel(const Table t, int scaled, float max_norm, float* norm) {
+  const uint32_t wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+  const bool busy = wave < t.groups;
+  const Tensor& x = t.t[find(t, busy ? wave : 0)];
+  const int64_t at = busy ? (int64_t)(wave - x.first) * kSmallChunk : 0;
+  const int n = busy ? (int)(x.n - at < kSmallChunk ? x.n - at : kSmallChunk) : 0;
+  double sum = 0.0;
+  auto square = [&](float v) { sum = __builtin_fma((double)v, (double)v, sum); };
+  if (x.gbf16) {
+    wave_each((const uint16_t*)x.g + at, n, [&](int, const uint16_t* e, int) {
+#pragma unroll
+      for (int l = 0; l < 8; ++l) square(wide<uint16_t>(e[l]));
+    });
+  } else {
+    wave_each((const float*)x.g + at, n, [&](int, const float* e, int) {
+#pragma unroll
+      for (int l = 0; l < 4; ++l) square(e[l]);
+    });
+  }
+  const double v = sqrt(group_sum<kSmallWaves>(sum));
+  if (threadIdx.x == 0) norm[0] = (float)v;
+  if (!scaled) return;
+  // (a wave writes what it alone has read)
+  const Factor f = factor(v, max_norm);
+  if (f.kept && x.g == x.out) return;
+  if (x.gbf16) {
+    const uint16_t* g = (const uint16_t*)x.g + at;
+    if (x.obf16) wave_scale(g, (uint16_t*)x.out + at, n, f.by);
+    else wave_scale(g, (float*)x.out + at, n, f.by);
+  } else {
+    const float* g = (const float*)x.g + at;
+    if (x.obf16) wave_scale(g, (uint16_t*)x.out + at, n, f.by);
+    else wave_scale(g, (float*)x.out + at, n, f.by);
   }
 }
 
 }  // namespace
 
+hipError_t launch_small(const Table& t, bool scaled, float max_norm, float* norm, hipStream_t s) {
+  hipLaunchKernelGGL(small_kernel, dim3(1), dim3(64 * kSmallWaves), 0, s, t, scaled ? 1 : 0, max_norm, norm);
+  return hipGetLastError();
+}
 hipError_t launch_squares(const Table& t, double* part, int64_t from, hipStream_t s) {
   hipLaunchKernelGGL(squares_kernel, dim3(t.groups), dim3(NT), 0, s, t, part + from);
   return hipGetLastError();

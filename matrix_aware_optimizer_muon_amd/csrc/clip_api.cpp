@@ -67,6 +67,14 @@ hipError_t tables(int num, const void* const* g, const int64_t* numel, const muo
   return hipSuccess;
 }
 
+// Whether one launch does (a workgroup that goes through more, or through many
+// small tensors, takes longer than two launches).
+bool small(int num, const int64_t* numel) {
+  int64_t groups = 0;
+  for (int i = 0; i < num && groups <= kSmallGroups; ++i) groups += (numel[i] + kSmallChunk - 1) / kSmallChunk;
+  return groups > 0 && groups <= kSmallGroups;
+}
+
 muon_status check(int num, const void* const* g, const int64_t* numel, const muon_dtype* dtypes, float* norm,
                   void* workspace, size_t workspace_bytes, int64_t* chunk, int64_t* groups) {
   int64_t total;
@@ -86,13 +94,14 @@ muon_status check(int num, const void* const* g, const int64_t* numel, const muo
 
 // Whether something that is written overlaps anything else.
 bool overlaps(int num, const void* const* g, const int64_t* numel, const muon_dtype* dtypes, void* const* out,
-              const muon_dtype* out_dtypes) {
+              const muon_dtype* out_dtypes, const float* norm) {
   struct Range {
     uintptr_t from, to;
     bool written;
   };
   std::vector<Range> r;
-  r.reserve(2 * (size_t)num);
+  r.reserve(2 * (size_t)num + 1);
+  r.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, true});
   for (int i = 0; i < num; ++i) {
     if (numel[i] == 0) continue;
     const uintptr_t a = (uintptr_t)g[i], b = (uintptr_t)out[i];
@@ -127,6 +136,9 @@ muon_status muon_grad_norm(int num, const void* const* g, const int64_t* numel, 
   int64_t chunk, groups;
   const muon_status bad = check(num, g, numel, dtypes, norm, workspace, workspace_bytes, &chunk, &groups);
   if (bad != MUON_OK) return bad;
+  if (small(num, numel))
+    return hip(tables(num, g, numel, dtypes, nullptr, nullptr, kSmallChunk,
+                      [&](const Table& t, int64_t) { return launch_small(t, false, 0.0f, norm, stream); }));
   double* const part = (double*)workspace;
   hipError_t e = tables(num, g, numel, dtypes, nullptr, nullptr, chunk,
                         [&](const Table& t, int64_t from) { return launch_squares(t, part, from, stream); });
@@ -148,10 +160,13 @@ muon_status muon_clip_grads(int num, const void* const* g, const int64_t* numel,
     if (out[i] == g[i] && out_dtypes[i] != dtypes[i]) return MUON_ERR_INVALID_ARGUMENT;
   }
   try {
-    if (overlaps(num, g, numel, dtypes, out, out_dtypes)) return MUON_ERR_INVALID_ARGUMENT;
+    if (overlaps(num, g, numel, dtypes, out, out_dtypes, norm)) return MUON_ERR_INVALID_ARGUMENT;
   } catch (const std::bad_alloc&) {
     return MUON_ERR_UNSUPPORTED;
   }
+  if (small(num, numel))
+    return hip(tables(num, g, numel, dtypes, out, out_dtypes, kSmallChunk,
+                      [&](const Table& t, int64_t) { return launch_small(t, true, max_norm, norm, stream); }));
   double* const part = (double*)workspace;
   hipError_t e = tables(num, g, numel, dtypes, nullptr, nullptr, chunk,
                         [&](const Table& t, int64_t from) { return launch_squares(t, part, from, stream); });

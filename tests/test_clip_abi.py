@@ -57,7 +57,7 @@ def test_header_and_binding_agree():
     ({"g": (P, P + 396)}, INVALID), ({"g": (P, P), "types": (0, 0)}, INVALID),      # what is written overlaps
     ({"out": (4 * P, 4 * P + 396)}, INVALID), ({"out": (2 * P + 396, 4 * P)}, INVALID),
     ({"g": (P, P), "types": (0, 0), "out": (P, 4 * P)}, INVALID),
-    ({"wsb": 8}, SMALL), ({"ws": 0}, INVALID), ({"ws": P + 8}, INVALID)])
+    ({"norm": P + 8}, INVALID), ({"wsb": 8}, SMALL), ({"ws": 0}, INVALID), ({"ws": P + 8}, INVALID)])
 def test_refusals(kw, want):
     assert call(**kw) == want
 
