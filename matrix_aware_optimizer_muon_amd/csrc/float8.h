@@ -66,8 +66,8 @@ hipError_t launch_sums(const MmParams& p, hipStream_t s);
 // partly filled one each), and one for rows of no expert.
 inline int64_t row_tiles(int64_t t, int64_t T, int64_t experts) { return t / T + (experts < t ? experts : t) + 1; }
 
-// The forward product for few rows of x (of each expert): `rows` (16 or 32) at
-// a time against 16 rows of w, which is read straight from memory.
+// The forward product for few rows of x (of each expert): `rows` (16, or 32 of
+// one matrix) at a time against 16 rows of w, which is read straight from memory.
 hipError_t launch_few(const MmParams& p, int rows, hipStream_t s);
 
 }  // namespace f8

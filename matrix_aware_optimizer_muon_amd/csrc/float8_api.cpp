@@ -28,6 +28,9 @@ muon_status hip(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_ERR_HIP;
 bool matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t size) {
   return p && aligned(p, size) && (rows <= 1 || ld >= cols);
 }
+// Distances that no memory holds, whose products would pass 64 bits.
+constexpr int64_t kFar = 1ll << 36;
+bool far(int64_t ld, int64_t rows) { return rows > 1 && (ld > kFar || ld < -kFar); }
 // 8-bit rows: each starts at a multiple of 16 bytes.  (Kernels add up a tile's
 // row distances in 32 bits: kMaxLd.)
 constexpr int64_t kMaxLd = 1ll << 24;
@@ -112,6 +115,7 @@ void choose_dense(Choice& c) {
     for (const int few : {16, 32})
       if (c.nq <= few && few_us(1.0, (double)c.nq, few, c.np, c.kd) < best) {
         c.few = few;
+        c.splits = 1;
         break;
       }
 }
@@ -218,14 +222,16 @@ muon_status run(const Call& v, hipStream_t s) {
   const int64_t o_rows = dw ? n : t, o_cols = fwd ? n : k;
   if (o_rows == 0 || o_cols == 0) return MUON_OK;
   if (!matrix(v.out, v.ldo, o_rows, o_cols, size_of(v.dtype))) return MUON_ERR_INVALID_ARGUMENT;
-  if ((fwd && t > 1 && v.lda > kMaxLd) || (b_rows > 1 && v.ldb > kMaxLd)) return MUON_ERR_UNSUPPORTED;
+  if ((fwd && t > 1 && v.lda > kMaxLd) || (b_rows > 1 && v.ldb > kMaxLd) || far(v.lda, t) || far(v.ldo, o_rows) ||
+      (dw ? far(v.o_stride, v.experts) : far(v.b_stride, v.experts)))
+    return MUON_ERR_UNSUPPORTED;
   if (t * a_cols > 0 && !(fwd ? matrix8(v.a, v.lda, t, a_cols) : matrix(v.a, v.lda, t, a_cols, 2)))
     return MUON_ERR_INVALID_ARGUMENT;
   if (b_rows * k > 0 && !matrix8(v.b, v.ldb, b_rows, k)) return MUON_ERR_INVALID_ARGUMENT;
   if ((fwd && t * k > 0 && !v.a_scale) || (b_rows * k > 0 && !v.b_scale)) return MUON_ERR_INVALID_ARGUMENT;
   if (v.experts > 1) {
     // one expert's matrix behind the other's
-    if (dw && v.o_stride < (o_rows - 1) * v.ldo + o_cols) return MUON_ERR_INVALID_ARGUMENT;
+    if (dw && v.o_stride < (o_rows > 1 ? (o_rows - 1) * v.ldo : 0) + o_cols) return MUON_ERR_INVALID_ARGUMENT;
     if (!dw && n * k > 0 && (v.b_stride % 16 || v.b_stride < (n > 1 ? (n - 1) * v.ldb : 0) + k))
       return MUON_ERR_INVALID_ARGUMENT;
   }
@@ -286,8 +292,9 @@ muon_status muon_f8_quantize(const void* x, int64_t ldx, int64_t x_stride, muon_
   const muon_status bad = form_sizes(dtype, count, rows, cols, block_rows);
   if (bad != MUON_OK) return bad;
   if (count == 0 || rows == 0 || cols == 0) return MUON_OK;
+  if (far(ldx, rows) || far(ldq, rows) || far(x_stride, count) || far(q_stride, count)) return MUON_ERR_UNSUPPORTED;
   if (!matrix(x, ldx, rows, cols, size_of(dtype)) || !matrix8(q, ldq, rows, cols) || !scale ||
-      (count > 1 && (q_stride % 16 || q_stride < (rows - 1) * ldq + cols)))
+      (count > 1 && (q_stride % 16 || q_stride < (rows > 1 ? (rows - 1) * ldq : 0) + cols)))
     return MUON_ERR_INVALID_ARGUMENT;
   const FormParams p = {(void*)x, q, scale, count, rows, cols, ldx, x_stride, ldq, q_stride, block_rows};
   return hip(launch_quantize(p, dtype == MUON_BF16, stream));
@@ -299,8 +306,9 @@ muon_status muon_f8_dequantize(const uint8_t* q, int64_t ldq, int64_t q_stride, 
   const muon_status bad = form_sizes(dtype, count, rows, cols, block_rows);
   if (bad != MUON_OK) return bad;
   if (count == 0 || rows == 0 || cols == 0) return MUON_OK;
+  if (far(ldx, rows) || far(ldq, rows) || far(x_stride, count) || far(q_stride, count)) return MUON_ERR_UNSUPPORTED;
   if (!matrix(x, ldx, rows, cols, size_of(dtype)) || !matrix8(q, ldq, rows, cols) || !scale ||
-      (count > 1 && (q_stride % 16 || x_stride < (rows - 1) * ldx + cols)))
+      (count > 1 && (q_stride % 16 || x_stride < (rows > 1 ? (rows - 1) * ldx : 0) + cols)))
     return MUON_ERR_INVALID_ARGUMENT;
   const FormParams p = {x, (uint8_t*)q, (uint8_t*)scale, count, rows, cols, ldx, x_stride, ldq, q_stride, block_rows};
   return hip(launch_dequantize(p, dtype == MUON_BF16, stream));
@@ -311,6 +319,7 @@ muon_status muon_f8_workspace(muon_f8_product product, const void* a, int64_t ld
   if (!workspace_bytes || !known(dtype)) return MUON_ERR_INVALID_ARGUMENT;
   const muon_status bad = product_sizes(product, grouped != 0, experts, t, n, k);
   if (bad != MUON_OK) return bad;
+  if (far(lda, t)) return MUON_ERR_UNSUPPORTED;
   *workspace_bytes = (size_t)choose(product, a, lda, grouped != 0, experts, t, n, k, dtype == MUON_BF16).bytes;
   return MUON_OK;
 }

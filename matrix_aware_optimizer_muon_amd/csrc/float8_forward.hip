@@ -526,7 +526,7 @@ hipError_t launch_few(const MmParams& p, int rows, hipStream_t s) {
     return hipGetLastError();
   };
   if (rows == 16) return p.ends ? go(few_kernel<true, 1, 8>, 8) : go(few_kernel<false, 1, 8>, 8);
-  if (rows == 32) return p.ends ? go(few_kernel<true, 2, 8>, 8) : go(few_kernel<false, 2, 8>, 8);
+  if (rows == 32 && !p.ends) return go(few_kernel<false, 2, 8>, 8);
   return hipErrorInvalidValue;
 }
 

@@ -219,8 +219,9 @@ __global__ void __launch_bounds__(256) back_kernel(const FormParams p, uint32_t 
 // another (a multiple of 128 of them, so that blocks stay whole).
 template <typename F>
 hipError_t in_parts(const FormParams& p, int64_t per_row, int64_t item, F f) {
-  constexpr int64_t kMost = 1ll << 30;
-  const int64_t matrix = p.rows * per_row;
+  constexpr int64_t kMost = 1ll << 28;
+  // (a launch has fewer than 2^32 threads, 256 for a block of 128 rows)
+  const int64_t matrix = (p.block_rows == kBlock ? (p.rows + kBlock - 1) / kBlock * kBlock : p.rows) * per_row;
   const int64_t many = std::max<int64_t>(1, kMost / matrix), some = std::max<int64_t>(1, kMost / per_row / kBlock) * kBlock;
   const int kb = (int)((p.cols + kBlock - 1) / kBlock), nb = (int)((p.rows + kBlock - 1) / kBlock);
   for (int64_t m = 0; m < p.count; m += many)

@@ -13,6 +13,7 @@ from matrix_aware_optimizer_muon_amd import float8 as f8
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(__file__)), "include", "muon_float8.h")
 OK, INVALID, UNSUPPORTED, SMALL = 0, 1, 2, 3
+FAR = 1 << 60  # a distance whose multiples pass 64 bits
 P = 1 << 20  # a non-null, 256-byte aligned address that is never read
 
 
@@ -31,7 +32,8 @@ def test_header_and_binding_agree():
     ({"block": 0}, INVALID), ({"rows": (1 << 24) + 1}, UNSUPPORTED), ({"cols": (1 << 24) + 1}, UNSUPPORTED),
     ({"x": 0}, INVALID), ({"x": P + 1}, INVALID), ({"ldx": 63}, INVALID), ({"q": 0}, INVALID), ({"q": P + 8}, INVALID),
     ({"ldq": 72}, INVALID), ({"ldq": 48}, INVALID), ({"scale": 0}, INVALID), ({"count": 2, "sq": 200, "sx": 400}, INVALID),
-    ({"count": 2, "sq": 264, "sx": 400}, INVALID)])
+    ({"count": 2, "sq": 264, "sx": 400}, INVALID), ({"ldx": FAR}, UNSUPPORTED), ({"ldq": FAR}, UNSUPPORTED),
+    ({"count": 2, "sq": FAR, "sx": 400}, UNSUPPORTED), ({"count": 2, "sq": 256, "sx": FAR}, UNSUPPORTED)])
 def test_form_refusals(kw, want):
     a = dict(x=P, ldx=64, sx=0, dtype=1, count=1, rows=4, cols=64, block=1, q=P, ldq=64, sq=0, scale=P)
     a.update(kw)
@@ -65,7 +67,8 @@ def product(kind, t=40, n=48, k=64, a=P, lda=None, sa=P, b=P, ldb=None, bs=None,
     ({"a": P + 1}, INVALID), ({"b": 0}, INVALID), ({"b": P + 8}, INVALID), ({"ldb": 72}, INVALID), ({"ldb": 48}, INVALID),
     ({"lda": 20}, INVALID), ({"out": 0}, INVALID), ({"out": P + 2}, INVALID), ({"ldo": 20}, INVALID), ({"sb": 0}, INVALID),
     ({"experts": 0}, INVALID), ({"experts": 2}, INVALID), ({"ends": P, "experts": 1025}, UNSUPPORTED),
-    ({"ends": P + 2, "experts": 2}, INVALID)])
+    ({"ends": P + 2, "experts": 2}, INVALID), ({"lda": FAR}, UNSUPPORTED), ({"ldb": FAR}, UNSUPPORTED),
+    ({"ldo": FAR}, UNSUPPORTED), ({"ends": P, "experts": 2, "bs": FAR, "os_": FAR}, UNSUPPORTED)])
 def test_product_refusals(kind, kw, want):
     assert product(kind, **kw) == want
 
@@ -102,6 +105,7 @@ def test_workspaces():
     assert f.muon_f8_workspace(0, P, 64, 0, 1, 40, 48, 64, 1, None) == INVALID
     assert f.muon_f8_workspace(3, P, 64, 0, 1, 40, 48, 64, 1, P) == INVALID
     assert f.muon_f8_workspace(0, P, 64, 0, 2, 40, 48, 64, 1, P) == INVALID
+    assert f.muon_f8_workspace(1, P, FAR, 0, 1, 40, 48, 64, 1, P) == UNSUPPORTED
 
 
 def f8_of(shape, square=False, cols=None):
