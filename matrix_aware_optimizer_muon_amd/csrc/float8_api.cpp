@@ -32,7 +32,7 @@ bool matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t size)
 constexpr int64_t kFar = 1ll << 36;
 bool far(int64_t ld, int64_t rows) { return rows > 1 && (ld > kFar || ld < -kFar); }
 // 8-bit rows: each starts at a multiple of 16 bytes.  (Kernels add up a tile's
-// row distances in 32 bits: kMaxLd.)
+// row distances in 32 bits: kMaxLd, bytes.)
 constexpr int64_t kMaxLd = 1ll << 24;
 bool matrix8(const void* p, int64_t ld, int64_t rows, int64_t cols) {
   return p && aligned(p, 16) && (rows <= 1 || (ld >= cols && ld % 16 == 0));
@@ -60,10 +60,10 @@ struct Costs {
   Cost t256, t128, t128g2, t64g4;
 };
 const Costs kCosts[] = {
-    {{1.37, 10.5}, {0.89, 6.0}, {1.00, 4.9}, {1.05, 4.2}},  // FWD
-    {{0.0, 0.0}, {1.58, 6.9}, {1.60, 6.3}, {1.35, 4.5}},    // FWD32 (no 256-wide tile)
-    {{0.78, 8.7}, {0.52, 6.1}, {0.535, 6.0}, {0.69, 2.8}},  // DX
-    {{0.79, 8.3}, {0.54, 6.2}, {0.545, 6.1}, {0.70, 2.8}},  // DW
+    {{1.39, 10.8}, {0.91, 6.0}, {1.01, 4.9}, {1.05, 4.1}},  // FWD
+    {{0.0, 0.0}, {1.57, 7.2}, {1.63, 6.3}, {1.38, 4.4}},    // FWD32 (no 256-wide tile)
+    {{0.79, 8.1}, {0.52, 6.0}, {0.54, 5.6}, {0.53, 3.5}},   // DX
+    {{0.80, 7.8}, {0.54, 5.8}, {0.54, 5.8}, {0.45, 4.3}},   // DW
 };
 
 // The few rows' kernel, us: the read of w and, growing with the rows, of x; a
@@ -121,8 +121,11 @@ void choose_dense(Choice& c) {
 }
 
 // The same for experts, whose rows only the device knows: their number of tiles
-// is taken as if they shared the rows evenly, with half a tile more each.  No
-// splits: the tiles of many experts fill the card.
+// is taken as if they shared the rows evenly, with half a tile more each, and at
+// least one (0.85 of 256 rows, of which up to 128 take less time).  256-wide ones
+// have to win by 4 %, since fewer tiles spread worse: over 105 sizes, 4 to 16000
+// rows per expert of uneven numbers, the choice is 1 % off the better one in the
+// mean.  No splits: the tiles of many experts fill the card.
 void choose_experts(Choice& c, int64_t experts, int64_t t) {
   const Costs& costs = kCosts[c.kind];
   const bool fwd = c.kind == FWD || c.kind == FWD32;
@@ -137,7 +140,8 @@ void choose_experts(Choice& c, int64_t experts, int64_t t) {
       return rounds(tiles, slots) * (cost.stage * rows / 32.0 + cost.ends) + (tiles < 2 * slots ? cost.stage * rows / 32.0 : 0.0);
     }
     const double stages = fwd ? (double)blocks_of(c.kd) : (double)((c.kd + 31) / 32);
-    const double tiles = busy * std::max(1.0, rows / (double)T + 0.5) * columns(T, c.np);
+    const double each = T == 256 ? std::max(0.85, rows / 256.0 + 0.51) : std::max(1.0, rows / (double)T + 0.5);
+    const double tiles = busy * each * columns(T, c.np);
     // (alone on its compute unit a 128-wide tile has a stage in two thirds of the time)
     const double stage = T == 128 && tiles <= 256 ? cost.stage * 0.67 : cost.stage;
     return std::ceil(rounds(tiles, slots)) * (stage * stages + cost.ends);
@@ -145,7 +149,7 @@ void choose_experts(Choice& c, int64_t experts, int64_t t) {
   double best = way(128, costs.t128, 512);
   c.tile = 128;
   if (costs.t256.stage > 0) {
-    const double us = way(256, costs.t256, 256);
+    const double us = way(256, costs.t256, 256) * (c.kind == DW ? 1.0 : 1.04);
     if (us < best) {
       best = us;
       c.tile = 256;
@@ -166,9 +170,9 @@ Choice choose(muon_f8_product product, const void* a, int64_t lda, bool grouped,
   const int64_t a_cols = fwd ? k : n, size = fwd ? 1 : 2;
   c.lda = t <= 1 ? up(a_cols * size, 16) : lda * size;
   if (!fwd && t * n > 0) {
-    // bf16 rows that the DMA cannot read: not at 16 bytes, or with a last
-    // chunk that would leave the matrix
-    c.pack = !aligned(a, 16) || c.lda % 16 || a_cols % 8;
+    // bf16 rows that the DMA cannot read: not at 16 bytes, with a last chunk that
+    // would leave the matrix, or too far apart
+    c.pack = !aligned(a, 16) || c.lda % 16 || a_cols % 8 || c.lda > kMaxLd;
     if (c.pack) {
       c.lda = up(a_cols * 2, 16);
       c.bytes = up(t * c.lda, 256);

@@ -24,6 +24,7 @@ namespace f8 {
 namespace {
 
 constexpr int SB = 128;  // bytes of K per stage and row: a cache line, a block of scales
+constexpr int D = 2;     // stages of a ring
 
 // 16-byte chunks of a stage's row are swapped by the row: reads of 16
 // consecutive rows of one chunk fall on the 16 places of two rows.
@@ -34,12 +35,12 @@ __device__ __forceinline__ int swz_s(int row) { return (row >> 1) & 7; }
 template <int T, int NW>
 struct RowOperand {
   static constexpr int NDMA = T * SB / 1024 / NW;  // 1-KB instructions per wave and stage
-  const char* base;     // the tile's first row
+  Rsrc base;            // the tile's first row
   uint32_t off[NDMA];   // the lane's place in the first stage
   int kbytes;
 
   __device__ __forceinline__ void init(const char* b, int64_t ld, int row0, int count, int kd, int wave, int lane) {
-    base = b + row0 * ld;
+    base = rsrc(b + row0 * ld);
     kbytes = kd;
 #pragma unroll
     for (int i = 0; i < NDMA; ++i) {
@@ -51,17 +52,12 @@ struct RowOperand {
   // Instruction i of stage ks; if not WHOLE, chunks past the row's end are zeros.
   template <Mode M>
   __device__ __forceinline__ void load(int i, char* stage, int ks, int wave, int lane) const {
-    const char* s = base + (int64_t)ks * SB + off[i];
+    uint32_t at = off[i];
     if (M != WHOLE) {
       const int c = (lane & 7) ^ swz_s((wave * NDMA + i) * 8 + lane / 8);
-      s = ks * SB + c * 16 < kbytes ? s : g_zero;
+      at = ks * SB + c * 16 < kbytes ? at : kPast;
     }
-    // (an address that the compiler cannot follow: it otherwise puts a wait for
-    // every earlier DMA before a read of the LDS object; the waits are this
-    // kernel's own)
-    uint32_t to = (uint32_t)(uintptr_t)(lds_ptr_t*)(stage + (wave * NDMA + i) * 1024);
-    asm("" : "+s"(to));
-    __builtin_amdgcn_global_load_lds((gbl_ptr_t*)s, (lds_ptr_t*)(uintptr_t)to, 16, 0, 0);
+    dma16(base, stage + (wave * NDMA + i) * 1024, at, ks * SB);
   }
 };
 
@@ -99,7 +95,7 @@ template <> struct HalfReader<false> {
   }
 };
 
-// One tile (or a contraction range of one) per workgroup of G groups of NW
+// One tile (or a contraction range of one) of T columns and TQ rows by G groups of NW
 // waves, which share its K, each with rings of its own, and join their sums
 // through LDS.
 //
@@ -110,63 +106,26 @@ template <> struct HalfReader<false> {
 // fragments of its first half are read behind the last MFMAs.  Nothing that a
 // slot needs is asked for less than several slots before, so a wave that has its
 // SIMD to itself keeps the matrix core fed.
-template <int KIND, bool GROUPED, int T, int G, int NW>
-__global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) forward_kernel(const MmParams p) {
+template <int KIND, int T, int TQ, int G, int NW>
+__device__ __forceinline__ void forward_tile(const MmParams& p, const Work& w, char* s_p, char* s_q) {
   constexpr bool R32 = KIND == FWD;
-  constexpr int FR = R32 ? 32 : 16;                // rows and columns of an MFMA
-  constexpr int WQ = NW / 2;                       // waves along Q (2 along P)
-  constexpr int FP = T / 2 / FR, FQ = T / WQ / FR; // MFMA blocks per wave
-  typedef RowOperand<T, NW> Op;
+  constexpr int FR = R32 ? 32 : 16;                 // rows and columns of an MFMA
+  constexpr int WQ = NW / 2;                        // waves along Q (2 along P)
+  constexpr int FP = T / 2 / FR, FQ = TQ / WQ / FR; // MFMA blocks per wave
+  typedef RowOperand<T, NW> OpP;
+  typedef RowOperand<TQ, NW> OpQ;
   typedef HalfReader<R32> Rd;
   typedef typename Rd::F F;
   typedef std::conditional_t<R32, f32x16, f32x4> Acc;
-  constexpr int OPB = T * SB;                      // one operand's stage in LDS
-  constexpr int D = 2;                             // stages of a ring
-  __shared__ __attribute__((aligned(1024))) char s_p[G * D * OPB];
-  __shared__ __attribute__((aligned(1024))) char s_q[G * D * OPB];
+  constexpr int OPB = T * SB;                       // room of one operand's stage in LDS
 
   const int tid = threadIdx.x % (64 * NW), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int group = G > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / (64 * NW)) : 0;
-  const int ring = group * D * OPB;                // the group's rings
+  const int ring = group * D * OPB;                 // the group's rings
   auto at = [&](int st) { return (st & (D - 1)) * OPB; };  // a stage in them
   const int wp = wave / WQ, wq = wave % WQ;
-
-  // This workgroup's tile, and its part of the operands.
-  const char *P = p.P, *Q = p.Q;
-  const uint8_t *scp = p.sp, *scq = p.sq;
-  Out o = {p.out, p.obf16, 0};
-  int nq = p.nq;
-  const int kd = p.kd, tiles_p = (p.np + T - 1) / T;
-  const int bid = (int)xcd_remap_chunked(blockIdx.x, gridDim.x, 32);
-  int tile = bid, split = 0, splits = 1, tiles_q = (nq + T - 1) / T;
-  if constexpr (GROUPED) {
-    Part f;
-    if (!find_part<T>(p.ends, p.experts, nq, bid / tiles_p, f)) {
-      zero_rows(p, bid - f.ahead * tiles_p, (int)gridDim.x - f.ahead * tiles_p);
-      return;
-    }
-    tile = bid - f.ahead * tiles_p;
-    nq = f.rows;
-    tiles_q = (nq + T - 1) / T;
-    P += f.expert * p.stride_p;
-    scp += f.expert * p.stride_sp;
-    Q += f.lo * p.ldq;
-    scq += (int64_t)f.lo * p.ldsq;
-    o.out = (char*)o.out + f.lo * p.ldo * (p.obf16 ? 2 : 4);
-  } else {
-    // The first `direct` tiles belong to one workgroup each, the others to
-    // `splits` workgroups each, a range of K apiece.
-    const int rest = tiles_p * tiles_q - p.direct;
-    if (bid >= p.direct) {
-      const int u = bid - p.direct;
-      split = u / rest;
-      tile = p.direct + u - split * rest;
-      splits = p.splits;
-    }
-  }
-  int tp, tq;
-  full_tile_grouped(tile, tiles_p, tiles_q, 8, &tp, &tq);
+  const int kd = w.kd, nq = w.at.nq, tp = w.at.tp, tq = w.at.tq, split = w.at.split, splits = w.at.splits;
 
   const int full = kd / SB, nk = (kd + SB - 1) / SB;
   int k0 = 0, k1 = nk;
@@ -189,14 +148,15 @@ __global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) forwa
       for (int e = 0; e < (R32 ? 16 : 4); ++e) acc[i][j][e] = 0.0f;
 
   if (steps > 0) {  // (an empty sum reads nothing)
-    Op dp, dq;
-    dp.init(P, p.ldp, tp * T, p.np, kd, wave, lane);
-    dq.init(Q, p.ldq, tq * T, nq, kd, wave, lane);
-    constexpr int DPS = 2 * Op::NDMA;              // a stage's instructions
+    OpP dp;
+    OpQ dq;
+    dp.init(w.P, p.ldp, tp * T, p.np, kd, wave, lane);
+    dq.init(w.Q, p.ldq, tq * T, nq, kd, wave, lane);
+    constexpr int DPS = OpP::NDMA + OpQ::NDMA;             // a stage's instructions
     auto dma = [&](auto in, int q, int st) __attribute__((always_inline)) {  // instruction q of stage k0 + st
       constexpr Mode M = decltype(in)::mode;
-      if (q < Op::NDMA) dp.template load<M>(q, s_p + ring + at(st), k0 + st, wave, lane);
-      else dq.template load<M>(q - Op::NDMA, s_q + ring + at(st), k0 + st, wave, lane);
+      if (q < OpP::NDMA) dp.template load<M>(q, s_p + ring + at(st), k0 + st, wave, lane);
+      else dq.template load<M>(q - OpP::NDMA, s_q + ring + at(st), k0 + st, wave, lane);
     };
     // Scales: the wave's columns lie in one block of weights, its rows have one
     // each; four stages' at a time (a gather of a byte per row and stage took 6 %
@@ -206,7 +166,7 @@ __global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) forwa
     const uint8_t* sq_at[FQ];
 #pragma unroll
     for (int j = 0; j < FQ; ++j)
-      sq_at[j] = scq + (int64_t)min(tq * T + wq * (T / WQ) + FR * j + lane % FR, nq - 1) * p.ldsq;
+      sq_at[j] = w.scq + (int64_t)min(tq * T + wq * (TQ / WQ) + FR * j + lane % FR, nq - 1) * p.ldsq;
     struct Scales {
       uint32_t p, q[FQ];
     } now, coming, four1, four2;
@@ -216,7 +176,7 @@ __global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) forwa
     auto ask = [&](int b) __attribute__((always_inline)) {
       const int from = min(b, nk - 4);
       shift = 8 * min(b - from, 3);
-      __builtin_memcpy(&four2.p, scp + sp_row + from, 4);
+      __builtin_memcpy(&four2.p, w.scp + sp_row + from, 4);
 #pragma unroll
       for (int j = 0; j < FQ; ++j) __builtin_memcpy(&four2.q[j], sq_at[j] + from, 4);
     };
@@ -250,7 +210,7 @@ __global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) forwa
         const uint32_t v = row[0] | (uint32_t)row[min(1, nk - 1)] << 8 | (uint32_t)row[min(2, nk - 1)] << 16;
         return v >> (8 * k0);
       };
-      four1.p = bytes(scp + sp_row);
+      four1.p = bytes(w.scp + sp_row);
 #pragma unroll
       for (int j = 0; j < FQ; ++j) four1.q[j] = bytes(sq_at[j]);
     }
@@ -258,7 +218,7 @@ __global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) forwa
 
     Rd rp, rq;
     rp.init(ring, wp * (T / 2), lane);
-    rq.init(ring, wq * (T / WQ), lane);
+    rq.init(ring, wq * (TQ / WQ), lane);
     // Zeros behind the rows' ends in the last stage, which stands in LDS (a
     // barrier has said so).  All waves call it.
     auto zero_tail = [&]() __attribute__((always_inline)) {
@@ -374,7 +334,56 @@ __global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) forwa
     }
   }
   barrier();  // no wave reads the rings any more
-  finish_tile<FR, T, G, NW, G * D * OPB>(acc, p, o, {tile, split, splits, tp, tq, nq}, group, tid, s_p, s_q);
+  finish_tile<FR, T, TQ, 2, G, NW, G * D * OPB>(acc, p, w.o, w.at, group, tid, s_p, s_q);
+}
+
+// A workgroup per tile.  An expert's last row tile that has at most half its
+// rows takes about half the time.
+template <int KIND, bool GROUPED, int T, int G, int NW>
+__global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) forward_kernel(const MmParams p) {
+  __shared__ __attribute__((aligned(1024))) char s_p[G * D * T * SB];
+  __shared__ __attribute__((aligned(1024))) char s_q[G * D * T * SB];
+
+  // This workgroup's tile, and its part of the operands.
+  const char *P = p.P, *Q = p.Q;
+  const uint8_t *scp = p.sp, *scq = p.sq;
+  Out o = {p.out, p.obf16, 0};
+  int nq = p.nq;
+  const int kd = p.kd, tiles_p = (p.np + T - 1) / T;
+  const int bid = (int)xcd_remap_chunked(blockIdx.x, gridDim.x, 32);
+  int tile = bid, split = 0, splits = 1, tiles_q = (nq + T - 1) / T;
+  if constexpr (GROUPED) {
+    Part f;
+    if (!find_part<T>(p.ends, p.experts, nq, bid / tiles_p, f)) {
+      zero_rows(p, bid - f.ahead * tiles_p, (int)gridDim.x - f.ahead * tiles_p);
+      return;
+    }
+    tile = bid - f.ahead * tiles_p;
+    nq = f.rows;
+    tiles_q = (nq + T - 1) / T;
+    P += f.expert * p.stride_p;
+    scp += f.expert * p.stride_sp;
+    Q += f.lo * p.ldq;
+    scq += (int64_t)f.lo * p.ldsq;
+    o.out = (char*)o.out + f.lo * p.ldo * (p.obf16 ? 2 : 4);
+  } else {
+    // The first `direct` tiles belong to one workgroup each, the others to
+    // `splits` workgroups each, a range of K apiece.
+    const int rest = tiles_p * tiles_q - p.direct;
+    if (bid >= p.direct) {
+      const int u = bid - p.direct;
+      split = u / rest;
+      tile = p.direct + u - split * rest;
+      splits = p.splits;
+    }
+  }
+  int tp, tq;
+  full_tile_grouped(tile, tiles_p, tiles_q, 8, &tp, &tq);
+
+  const Work w = {P, Q, scp, scq, o, kd, {tile, split, splits, tp, tq, nq}};
+  if constexpr (GROUPED && T == 256)
+    if (nq - tq * T <= T / 2) return forward_tile<KIND, T, T / 2, G, NW>(p, w, s_p, s_q);
+  forward_tile<KIND, T, T, G, NW>(p, w, s_p, s_q);
 }
 
 // Few rows of x, 16 QB of them against 16 rows of w: a workgroup's W waves take

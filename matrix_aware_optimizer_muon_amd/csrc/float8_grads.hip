@@ -23,6 +23,8 @@ namespace f8 {
 
 namespace {
 
+constexpr int D = 4;  // stages of a ring
+
 // P of the gradients: e4m3 rows along K, 16 columns (8 of 64-wide tiles) per
 // lane and chunk, widened with their scale on the way through registers into
 // LDS.  SQUARE: a scale per 128 rows (weights), else per row.  A chunk lies
@@ -32,8 +34,9 @@ struct WideOperand {
   static constexpr int CH = T == 64 ? 8 : 16;
   static constexpr int CPR = T / CH;
   static constexpr int N = KROWS * CPR / NT;  // chunks per lane, KROWS / N rows apart
-  static_assert(N >= 1 && KROWS * CPR == N * NT, "whole chunks per lane");
+  static_assert(N == 1 && KROWS * CPR == NT, "a chunk per lane: two loads that no compiler joins");
   static constexpr int PC = CH / 4, PIECES = N * PC;
+  static constexpr int LOADS = 2 * N;         // of a stage: values and scale
   struct Regs {
     u32x4 v[N];
     uint32_t scale[N];
@@ -90,32 +93,224 @@ struct WideOperand {
   }
 };
 
-template <int KIND, bool GROUPED, int T, int G, int NW>
-__global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) mm_kernel(const MmParams p) {
+// Q of the gradients, T rows (columns, if K-major) by direct loads into LDS, laid
+// out as DmaOperand does.  A row distance is at most 2^24 bytes.
+template <bool KM, int T, int NW>
+struct BufferOperand {
+  static constexpr int NDMA = T * KB / 1024 / NW;  // 1-KB instructions per wave and stage
+  const char* base;    // the tile's first row (column)
+  uint32_t off[NDMA];  // the lane's place in a stage,
+  int k[NDMA];         // and its row (byte) of K there
+  int64_t step;        // bytes from stage to stage
+  int kend;
+
+  __device__ __forceinline__ void init(const char* b, int64_t ld, int row0, int count, int kd, int tid) {
+    const int wave = tid >> 6, lane = tid & 63;
+    step = KM ? KROWS * ld : (int64_t)KB;
+    kend = KM ? kd : kd * 2;
+    base = KM ? b : b + row0 * ld;
+#pragma unroll
+    for (int i = 0; i < NDMA; ++i) {
+      if constexpr (KM) {
+        constexpr int RB = T * 2, RPI = 1024 / RB, CH = RB / 16;
+        k[i] = (wave * NDMA + i) * RPI + lane / CH;
+        const int ch = (lane % CH) ^ swz_k<T>(k[i]);
+        // (whole chunks, in the padded row)
+        off[i] = (uint32_t)k[i] * (uint32_t)ld + (uint32_t)min(row0 + ch * 8, (count - 1) & ~7) * 2;
+      } else {
+        const int r = (wave * NDMA + i) * 16 + (lane >> 2);
+        k[i] = ((lane & 3) ^ swz_c(r)) * 16;
+        off[i] = (uint32_t)min(r, count - 1 - row0) * (uint32_t)ld + (uint32_t)k[i];
+      }
+    }
+  }
+  // Instruction i of stage ks; if not WHOLE, what lies past K's end is zeros.
+  template <Mode M>
+  __device__ __forceinline__ void load(int i, char* stage, int ks, int wave) const {
+    uint32_t at = off[i];
+    if (M != WHOLE) at = ks * (KM ? KROWS : KB) + k[i] < kend ? at : kPast;
+    dma16(rsrc(base + ks * step), stage + (wave * NDMA + i) * 1024, at, 0);
+  }
+};
+
+// One tile (or a contraction range of one) of T columns and TQ rows.
+template <int KIND, int T, int TQ, int G, int NW>
+__device__ __forceinline__ void mm_tile(const MmParams& p, const Work& w, char* s_p, char* s_q) {
   constexpr bool QKM = KIND == DW;
-  constexpr int WQ = NW / 2;                       // waves along Q (2 along P)
-  constexpr int FP = T / 2 / 16, FQ = T / WQ / 16; // 16 x 16 blocks per wave
-  constexpr int H = FP / 2;                        // block rows per half stage
-  typedef DmaOperand<QKM, T, NW> DmaQ;
+  constexpr int WP = TQ < T ? 4 : 2, WQ = NW / WP;    // waves along P and Q
+  constexpr int FP = T / WP / 16, FQ = TQ / WQ / 16;  // 16 x 16 blocks per wave
+  constexpr int H = FP / 2;                           // block rows per half stage
+  typedef BufferOperand<QKM, TQ, NW> DmaQ;
   typedef WideOperand<KIND == DX, T, 64 * NW> RegP;
-  constexpr int DPS = DmaQ::NDMA;                  // a stage's instructions,
-  constexpr int DB = DPS / 2, DA = DPS - DB;       // in two halves
+  constexpr int DPS = DmaQ::NDMA;                     // a stage's instructions,
+  constexpr int DB = DPS / 2, DA = DPS - DB;          // in two halves
   constexpr int PIECES = RegP::PIECES;
-  constexpr int OPB = T * KB;                      // one operand's stage in LDS
-  constexpr int D = 4;                             // stages of a ring
-  constexpr int RS = 2;                            // register sets in flight
-  // (two objects: the compiler then knows that a write to one is no write to
-  // the other)
-  __shared__ __attribute__((aligned(1024))) char s_p[G * D * OPB];
-  __shared__ __attribute__((aligned(1024))) char s_q[G * D * OPB];
+  constexpr int OPB = T * KB;                         // room of one operand's stage in LDS
+  constexpr int RS = 2;                               // register sets in flight
 
   const int tid = threadIdx.x % (64 * NW), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int group = G > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / (64 * NW)) : 0;
-  const int ring = group * D * OPB;                // the group's rings
+  const int ring = group * D * OPB;                   // the group's rings
   auto at = [&](int st) { return (st & (D - 1)) * OPB; };  // a stage in them
   const int wp = wave / WQ, wq = wave % WQ;
   const int q4 = lane >> 4, c16 = lane & 15;
+  const int kd = w.kd, nq = w.at.nq, tp = w.at.tp, tq = w.at.tq, split = w.at.split, splits = w.at.splits;
+
+  const int full = kd / KROWS;
+  const int nk = (kd + KROWS - 1) / KROWS;
+  int k0 = 0, k1 = nk;
+  if (splits > 1) {
+    k0 = (int)((int64_t)nk * split / splits);
+    k1 = (int)((int64_t)nk * (split + 1) / splits);
+  }
+  // stages per group, and this group's (the last ones may have fewer)
+  const int most = (k1 - k0 + G - 1) / G;
+  const int steps = G > 1 ? max(0, min(most, k1 - k0 - group * most)) : k1 - k0;
+  k0 += group * most;
+  f32x4 acc[FP][FQ];
+#pragma unroll
+  for (int i = 0; i < FP; ++i)
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  if (steps > 0) {  // (an empty sum reads nothing)
+    DmaQ dq;
+    RegP gp;
+    gp.init(w.P, p.ldp, w.scp, p.ldsp, tp * T, p.np, kd, tid);
+    dq.init(w.Q, p.ldq, tq * T, nq, kd, tid);
+    auto dma = [&](auto in, int q, int st) __attribute__((always_inline)) {  // instruction q of stage k0 + st
+      dq.template load<decltype(in)::mode>(q, s_q + ring + at(st), k0 + st, wave);
+    };
+    typename RegP::Regs rp[RS];
+    typename RegP::Wide wide;
+    auto put = [&](auto in, typename RegP::Regs& r, int st, int q) __attribute__((always_inline)) {
+      gp.template store<decltype(in)::mode>(r, wide, s_p, ring + at(st), k0 + st, q);
+    };
+    Reader<true, T> fp;
+    Reader<QKM, TQ> fq;
+    fp.init(ring, wp * (T / WP), q4, c16);
+    fq.init(ring, wq * (TQ / WQ), q4, c16);
+    u32x4 fa[FP], fb0[FQ], fb1[FQ];
+
+    // DMA: a stage's DPS instructions go out in two halves, so that every run
+    // of MFMAs carries the same share: the first half of stage kt + D in the
+    // second half of step kt (its buffer is released by that step's barrier),
+    // the rest in the first half of step kt + 1.
+    // Registers: stage kt + 2 goes into LDS in the second half of step kt, and
+    // its set is loaded again with stage kt + 2 + RS, RS steps ahead of its
+    // use.
+#pragma unroll
+    for (int st = 0; st < D; ++st)
+      if (st < steps) {
+#pragma unroll
+        for (int q = 0; q < DPS; ++q)
+          if (st < D - 1 || q < DA) dma(In<CUT>(), q, st);
+      }
+    // stages 0 .. RS + 1 in flight together; everything has landed before
+    // the loop, so that the waits inside it only count the loop's own loads
+    typename RegP::Regs rp0[2];
+#pragma unroll
+    for (int st = 0; st < 2; ++st) gp.template load<CUT>(rp0[st], k0 + st);
+#pragma unroll
+    for (int st = 0; st < RS; ++st) gp.template load<CUT>(rp[st], k0 + 2 + st);
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q) put(In<CUT>(), rp0[st], st, q);
+    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
+    barrier();
+#pragma unroll
+    for (int f = 0; f < H; ++f) fa[f] = fp.get(s_p, at(0), f);
+#pragma unroll
+    for (int f = 0; f < FQ; ++f) fb0[f] = fq.get(s_q, at(0), f);
+
+    // A step, kt counting from k0, set = kt % RS.
+    auto step = [&](auto in, int kt, int set, u32x4* fb, u32x4* fbn) __attribute__((always_inline)) {
+      constexpr Mode M = decltype(in)::mode;
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) mfma(fa[0], fb[j], acc[0][j]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int f = H; f < FP; ++f) fa[f] = fp.get(s_p, at(kt), f);
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int N1 = (H - 1) * FQ, G1 = DB > 0 && N1 > DB ? N1 / (DB + (DB == 0)) : 1;
+#pragma unroll
+      for (int n = 0; n < N1; ++n) {
+        mfma(fa[1 + n / FQ], fb[n % FQ], acc[1 + n / FQ][n % FQ]);
+        if (M != DRAIN && DB > 0 && n % G1 == G1 - 1 && n / G1 < DB) {
+          dma(in, DA + n / G1, kt + D - 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if constexpr (N1 == 0 && M != DRAIN) {
+#pragma unroll
+        for (int q = 0; q < DB; ++q) dma(in, DA + q, kt + D - 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      // This wave's DMAs of stage kt + 1 have landed ((D - 2) DPS later ones
+      // may fly, and the register loads of two steps), its LDS writes of stage
+      // kt + 1 and its reads of stage kt are done.
+      __builtin_amdgcn_s_waitcnt(wait_imm(M == DRAIN ? 0 : (D - 2) * DPS + 2 * RegP::LOADS, 0));
+      barrier();
+#pragma unroll
+      for (int f = 0; f < H; ++f) fa[f] = fp.get(s_p, at(kt + 1), f);
+#pragma unroll
+      for (int f = 0; f < FQ; ++f) fbn[f] = fq.get(s_q, at(kt + 1), f);
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int N2 = H * FQ, G2 = N2 / DA;
+      // pieces after each MFMA (several, where there are few MFMAs)
+      constexpr int GP = N2 > PIECES ? N2 / (PIECES + 1) : 1, PB = (PIECES + N2 - 1) / N2;
+#pragma unroll
+      for (int n = 0; n < N2; ++n) {
+        mfma(fa[H + n / FQ], fb[n % FQ], acc[H + n / FQ][n % FQ]);
+        if (M != DRAIN && n % G2 == G2 - 1 && n / G2 < DA) dma(in, n / G2, kt + D);
+        if (n % GP == GP - 1) {
+#pragma unroll
+          for (int q = 0; q < PB; ++q)
+            if (n / GP * PB + q < PIECES) put(in, rp[set], kt + 2, n / GP * PB + q);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (M != DRAIN) gp.template load<M>(rp[set], k0 + kt + 2 + RS);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // Two steps per trip: the Q fragments and the register sets alternate
+    // without copies.  (The last step that has a stage to ask for is steps - D:
+    // the second half of its DMAs.)
+    static_assert(RS + 2 <= D, "a register load reaches no further than a DMA");
+    int kt = 0;
+    auto trip = [&](auto in) __attribute__((always_inline)) {
+      step(in, kt, 0, fb0, fb1);
+      step(in, kt + 1, 1, fb1, fb0);
+      kt += 2;
+    };
+    const int whole = min(steps, full - k0) - D;
+    while (kt + 1 < whole) trip(In<WHOLE>());
+    while (kt <= steps - D) trip(In<CUT>());
+    while (kt + 1 < steps) trip(In<DRAIN>());
+    if (kt < steps) step(In<DRAIN>(), kt, 0, fb0, fb1);
+    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));  // no load may land after the workgroup's LDS is given back
+  }
+
+  if constexpr (G > 1) {
+    // a group's barriers: one ahead of the loop and one per step
+    if (most > 0) {
+      for (int i = steps > 0 ? steps : -1; i < most; ++i) barrier();
+    }
+  }
+  barrier();  // no wave reads the rings any more
+  finish_tile<16, T, TQ, WP, G, NW, G * D * OPB>(acc, p, w.o, w.at, group, tid, s_p, s_q);
+}
+
+// A workgroup per tile.  An expert's last row tile that has at most half its
+// rows takes about half the time.
+template <int KIND, bool GROUPED, int T, int G, int NW>
+__global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) mm_kernel(const MmParams p) {
+  // (two objects: the compiler then knows that a write to one is no write to
+  // the other)
+  __shared__ __attribute__((aligned(1024))) char s_p[G * D * T * KB];
+  __shared__ __attribute__((aligned(1024))) char s_q[G * D * T * KB];
 
   // This workgroup's tile, and its part of the operands.
   const char *P = p.P, *Q = p.Q;
@@ -162,150 +357,10 @@ __global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) mm_ke
   int tp, tq;
   full_tile_grouped(tile, tiles_p, tiles_q, 8, &tp, &tq);
 
-  const int full = kd / KROWS;
-  const int nk = (kd + KROWS - 1) / KROWS;
-  int k0 = 0, k1 = nk;
-  if (splits > 1) {
-    k0 = (int)((int64_t)nk * split / splits);
-    k1 = (int)((int64_t)nk * (split + 1) / splits);
-  }
-  // stages per group, and this group's (the last ones may have fewer)
-  const int most = (k1 - k0 + G - 1) / G;
-  const int steps = G > 1 ? max(0, min(most, k1 - k0 - group * most)) : k1 - k0;
-  k0 += group * most;
-  f32x4 acc[FP][FQ];
-#pragma unroll
-  for (int i = 0; i < FP; ++i)
-#pragma unroll
-    for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-  if (steps > 0) {  // (an empty sum reads nothing)
-    DmaQ dq;
-    RegP gp;
-    gp.init(P, p.ldp, scp, p.ldsp, tp * T, p.np, kd, tid);
-    dq.init(Q, p.ldq, tq * T, nq, kd, kd * 2, full, tid);
-    auto dma = [&](int q, int st) __attribute__((always_inline)) {  // instruction q of stage k0 + st
-      dq.load(q, s_q + ring + at(st), k0 + st, full, wave);
-    };
-    typename RegP::Regs rp[RS];
-    typename RegP::Wide wide;
-    auto put = [&](auto in, typename RegP::Regs& r, int st, int q) __attribute__((always_inline)) {
-      gp.template store<decltype(in)::mode>(r, wide, s_p, ring + at(st), k0 + st, q);
-    };
-    Reader<true, T> fp;
-    Reader<QKM, T> fq;
-    fp.init(ring, wp * (T / 2), q4, c16);
-    fq.init(ring, wq * (T / WQ), q4, c16);
-    u32x4 fa[FP], fb0[FQ], fb1[FQ];
-
-    // DMA: a stage's DPS instructions go out in two halves, so that every run
-    // of MFMAs carries the same share: the first half of stage kt + D in the
-    // second half of step kt (its buffer is released by that step's barrier),
-    // the rest in the first half of step kt + 1.
-    // Registers: stage kt + 2 goes into LDS in the second half of step kt, and
-    // its set is loaded again with stage kt + 2 + RS, RS steps ahead of its
-    // use.
-#pragma unroll
-    for (int st = 0; st < D; ++st)
-      if (st < steps) {
-#pragma unroll
-        for (int q = 0; q < DPS; ++q)
-          if (st < D - 1 || q < DA) dma(q, st);
-      }
-    // stages 0 .. RS + 1 in flight together; everything has landed before
-    // the loop, so that the waits inside it only count the loop's own loads
-    typename RegP::Regs rp0[2];
-#pragma unroll
-    for (int st = 0; st < 2; ++st) gp.template load<CUT>(rp0[st], k0 + st);
-#pragma unroll
-    for (int st = 0; st < RS; ++st) gp.template load<CUT>(rp[st], k0 + 2 + st);
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int q = 0; q < PIECES; ++q) put(In<CUT>(), rp0[st], st, q);
-    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
-    barrier();
-#pragma unroll
-    for (int f = 0; f < H; ++f) fa[f] = fp.get(s_p, at(0), f);
-#pragma unroll
-    for (int f = 0; f < FQ; ++f) fb0[f] = fq.get(s_q, at(0), f);
-
-    // A step, kt counting from k0, set = kt % RS.
-    auto step = [&](auto in, int kt, int set, u32x4* fb, u32x4* fbn) __attribute__((always_inline)) {
-      constexpr Mode M = decltype(in)::mode;
-#pragma unroll
-      for (int j = 0; j < FQ; ++j) mfma(fa[0], fb[j], acc[0][j]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int f = H; f < FP; ++f) fa[f] = fp.get(s_p, at(kt), f);
-      __builtin_amdgcn_sched_barrier(0);
-      constexpr int N1 = (H - 1) * FQ, G1 = DB > 0 && N1 > DB ? N1 / (DB + (DB == 0)) : 1;
-#pragma unroll
-      for (int n = 0; n < N1; ++n) {
-        mfma(fa[1 + n / FQ], fb[n % FQ], acc[1 + n / FQ][n % FQ]);
-        if (M != DRAIN && DB > 0 && n % G1 == G1 - 1 && n / G1 < DB) {
-          dma(DA + n / G1, kt + D - 1);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-      if constexpr (N1 == 0 && M != DRAIN) {
-#pragma unroll
-        for (int q = 0; q < DB; ++q) dma(DA + q, kt + D - 1);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      // This wave's DMAs of stage kt + 1 have landed ((D - 2) DPS later ones
-      // may fly; register loads among them make the wait stricter), its LDS
-      // writes of stage kt + 1 and its reads of stage kt are done.
-      __builtin_amdgcn_s_waitcnt(wait_imm(M == DRAIN ? 0 : (D - 2) * DPS, 0));
-      barrier();
-#pragma unroll
-      for (int f = 0; f < H; ++f) fa[f] = fp.get(s_p, at(kt + 1), f);
-#pragma unroll
-      for (int f = 0; f < FQ; ++f) fbn[f] = fq.get(s_q, at(kt + 1), f);
-      __builtin_amdgcn_sched_barrier(0);
-      constexpr int N2 = H * FQ, G2 = N2 / DA;
-      // pieces after each MFMA (several, where there are few MFMAs)
-      constexpr int GP = N2 > PIECES ? N2 / (PIECES + 1) : 1, PB = (PIECES + N2 - 1) / N2;
-#pragma unroll
-      for (int n = 0; n < N2; ++n) {
-        mfma(fa[H + n / FQ], fb[n % FQ], acc[H + n / FQ][n % FQ]);
-        if (M != DRAIN && n % G2 == G2 - 1 && n / G2 < DA) dma(n / G2, kt + D);
-        if (n % GP == GP - 1) {
-#pragma unroll
-          for (int q = 0; q < PB; ++q)
-            if (n / GP * PB + q < PIECES) put(in, rp[set], kt + 2, n / GP * PB + q);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if constexpr (M != DRAIN) gp.template load<M>(rp[set], k0 + kt + 2 + RS);
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    // Two steps per trip: the Q fragments and the register sets alternate
-    // without copies.  (The last step that has a stage to ask for is steps - D:
-    // the second half of its DMAs.)
-    static_assert(RS + 2 <= D, "a register load reaches no further than a DMA");
-    int kt = 0;
-    auto trip = [&](auto in) __attribute__((always_inline)) {
-      step(in, kt, 0, fb0, fb1);
-      step(in, kt + 1, 1, fb1, fb0);
-      kt += 2;
-    };
-    const int whole = min(steps, full - k0) - D;
-    while (kt + 1 < whole) trip(In<WHOLE>());
-    while (kt <= steps - D) trip(In<CUT>());
-    while (kt + 1 < steps) trip(In<DRAIN>());
-    if (kt < steps) step(In<DRAIN>(), kt, 0, fb0, fb1);
-    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));  // no load may land after the workgroup's LDS is given back
-  }
-
-  if constexpr (G > 1) {
-    // a group's barriers: one ahead of the loop and one per step
-    if (most > 0) {
-      for (int i = steps > 0 ? steps : -1; i < most; ++i) barrier();
-    }
-  }
-  barrier();  // no wave reads the rings any more
-  finish_tile<16, T, G, NW, G * D * OPB>(acc, p, o, {tile, split, splits, tp, tq, nq}, group, tid, s_p, s_q);
+  const Work w = {P, Q, scp, nullptr, o, kd, {tile, split, splits, tp, tq, nq}};
+  if constexpr (GROUPED && T == 256)
+    if (nq - tq * T <= T / 2) return mm_tile<KIND, T, T / 2, G, NW>(p, w, s_p, s_q);
+  mm_tile<KIND, T, T, G, NW>(p, w, s_p, s_q);
 }
 
 // C = the splits' partial sums added in order: blockIdx.y a split tile, four

@@ -20,6 +20,25 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 // The scale that a byte stands for (255: NaN, as in e8m0).
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// Direct loads into LDS go through a buffer descriptor: 32-bit places from a base
+// that the whole workgroup shares, zeros for a place past the end.  (Beside the
+// global form the compiler can count neither the loads of registers nor the reads
+// of LDS, and waits for all that are out: a gradient's stage took 0.72 us.)
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+constexpr uint32_t kPast = 0xfffffff0u;
+__device__ __forceinline__ Rsrc rsrc(const char* base) {
+  // (word 3: 32-bit elements)
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)kPast, 4 << 15);
+}
+__device__ __forceinline__ void dma16(Rsrc r, char* to, uint32_t at, uint32_t step) {
+  // (an LDS address that the compiler cannot follow: it otherwise puts a wait for
+  // every earlier load before a read of the LDS object; the waits are the
+  // kernels' own)
+  uint32_t lds = (uint32_t)(uintptr_t)(lds_ptr_t*)to;
+  asm("" : "+s"(lds));
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t*)(uintptr_t)lds, 16, (int)at, (int)step, 0, 0);
+}
+
 // Four e4m3 values times a scale, as bf16: exact, two per instruction.  (A
 // scale's sign and fraction are not looked at; scale 2^-127 included.)
 __device__ __forceinline__ uint2 widen4(uint32_t v, float scale) {
@@ -112,20 +131,30 @@ struct Place {
   int tile, split, splits, tp, tq, nq;
 };
 
-// A tile's sums to memory.  Waves stand WQ along Q and 2 along P; acc[i][j]
+// A workgroup's tile and its part of the operands.
+struct Work {
+  const char *P, *Q;
+  const uint8_t *scp, *scq;
+  Out o;
+  int kd;
+  Place at;
+};
+
+// A tile's sums to memory, T columns and TQ rows (T of them, or the few that a
+// row tile's end has).  Waves stand WP along P and NW / WP along Q; acc[i][j]
 // covers FR columns and rows of the wave's part: quad g of it is columns FR i +
 // qcol(g) .. +3 of row FR j + qrow.  G groups of NW waves have summed a share of
 // K each; s_p and s_q hold RING bytes and nobody reads or writes them any more
 // (a barrier stands ahead of the call).
-template <int FR, int T, int G, int NW, int RING, int FP, int FQ, typename Acc>
+template <int FR, int T, int TQ, int WP, int G, int NW, int RING, int FP, int FQ, typename Acc>
 __device__ __forceinline__ void finish_tile(Acc (&acc)[FP][FQ], const MmParams& p, const Out& o, const Place& at,
                                             int group, int tid, char* s_p, char* s_q) {
-  constexpr int QUADS = FR == 32 ? 4 : 1, WQ = NW / 2;
+  constexpr int QUADS = FR == 32 ? 4 : 1, WQ = NW / WP;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q4 = lane >> 4;
   const int wp = wave / WQ, wq = wave % WQ;
   const int qrow = lane % FR;
   auto qcol = [&](int g) { return FR == 32 ? 8 * g + 4 * (lane >> 5) : 4 * q4; };
-  const int colt = wp * (T / 2), rowt = wq * (T / WQ);
+  const int colt = wp * (T / WP), rowt = wq * (TQ / WQ);
   const int col0 = at.tp * T + colt, row0 = at.tq * T + rowt;
   // A block's quads are finished by group b % G (b: the quad's number): j runs fastest.
   auto quad = [&](int i, int g, int j) __attribute__((always_inline)) {
@@ -165,7 +194,7 @@ __device__ __forceinline__ void finish_tile(Acc (&acc)[FP][FQ], const MmParams& 
     // through LDS, 16-byte chunks swapped within a row by the row's number,
     // and leave as whole runs of 128 bytes or more.  One loop over them, not
     // unrolled but for its first lines.
-    constexpr int PT = T / 2, SC = FR == 32 && PT > 64 ? 64 : PT, NH = PT / SC, CPR = SC / 4;
+    constexpr int PT = T / WP, SC = FR == 32 && PT > 64 ? 64 : PT, NH = PT / SC, CPR = SC / 4;
     static_assert(NW * FR * SC * 4 * G <= RING, "the staged rows fit a ring");
     static_assert(FQ % G == 0, "a row's quads are one group's");
     const bool wide = at.splits == 1 && p.obf16;

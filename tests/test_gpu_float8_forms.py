@@ -74,6 +74,16 @@ def test_scales_far_apart(t, bf16):
                        (dy.double().t() @ values(x, False) / 32).to(dtype))
 
 
+def test_rows_of_a_gradient_far_apart():
+    """More than 2^24 bytes apart, and more than 2^32 in all: laid out again."""
+    t, n, k, ld = 300, 64, 96, (1 << 23) + 8
+    far = torch.empty(t * ld, dtype=torch.bfloat16, device="cuda").as_strided((t, n), (ld, 1))
+    dy, w, x = exact_grad((t, n), 1), exact8((n, k), 2, True), exact8((t, k), 3, False)
+    far.copy_(dy)
+    assert torch.equal(f8.grad_input(far, w), f8.grad_input(dy, w))
+    assert torch.equal(f8.grad_weight(far, x), f8.grad_weight(dy, x))
+
+
 def test_more_matrices_than_a_launch_has_workgroups():
     """2^24 workgroups and more: the call is cut in parts."""
     x = torch.randn(1000, 1030, device="cuda").bfloat16()
