@@ -122,10 +122,11 @@ void choose_dense(Choice& c) {
 
 // The same for experts, whose rows only the device knows: their number of tiles
 // is taken as if they shared the rows evenly, with half a tile more each, and at
-// least one (0.85 of 256 rows, of which up to 128 take less time).  256-wide ones
-// have to win by 4 %, since fewer tiles spread worse: over 105 sizes, 4 to 16000
-// rows per expert of uneven numbers, the choice is 1 % off the better one in the
-// mean.  No splits: the tiles of many experts fill the card.
+// least one (0.45 and 0.75 of 256 rows, of which up to 128 take less time), and
+// no whole rounds: 0.4 of one more than their share.  256-wide ones have to win by
+// 4 %, since fewer tiles spread worse: over 105 sizes, 4 to 4000 rows per expert of
+// uneven numbers, the choice is 1 % off the better one in the mean.  No splits: the
+// tiles of many experts fill the card.
 void choose_experts(Choice& c, int64_t experts, int64_t t) {
   const Costs& costs = kCosts[c.kind];
   const bool fwd = c.kind == FWD || c.kind == FWD32;
@@ -140,11 +141,11 @@ void choose_experts(Choice& c, int64_t experts, int64_t t) {
       return rounds(tiles, slots) * (cost.stage * rows / 32.0 + cost.ends) + (tiles < 2 * slots ? cost.stage * rows / 32.0 : 0.0);
     }
     const double stages = fwd ? (double)blocks_of(c.kd) : (double)((c.kd + 31) / 32);
-    const double each = T == 256 ? std::max(0.85, rows / 256.0 + 0.51) : std::max(1.0, rows / (double)T + 0.5);
+    const double each = T == 256 ? std::max(0.75, rows / 256.0 + 0.45) : std::max(1.0, rows / (double)T + 0.5);
     const double tiles = busy * each * columns(T, c.np);
     // (alone on its compute unit a 128-wide tile has a stage in two thirds of the time)
     const double stage = T == 128 && tiles <= 256 ? cost.stage * 0.67 : cost.stage;
-    return std::ceil(rounds(tiles, slots)) * (stage * stages + cost.ends);
+    return (tiles > 0.8 * slots ? rounds(tiles + 0.4 * slots, slots) : 1.0) * (stage * stages + cost.ends);
   };
   double best = way(128, costs.t128, 512);
   c.tile = 128;

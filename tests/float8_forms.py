@@ -14,13 +14,13 @@ SIZES = [
     (0, 1, 0, 65, 8565, 682), (0, 0, 0, 886, 1156, 619), (0, 1, 0, 34, 66, 3332), (0, 0, 0, 795, 1280, 2820),
     (0, 1, 0, 3776, 1030, 678), (0, 0, 0, 6595, 591, 646), (0, 1, 0, 2681, 3200, 3380), (0, 0, 0, 3425, 2365, 785),
     (0, 1, 0, 5952, 1418, 645), (0, 1, 0, 4754, 6882, 698), (0, 1, 7, 1000, 300, 605), (0, 0, 7, 1000, 300, 613),
-    (0, 1, 4, 1714, 4288, 612),
+    (0, 1, 18, 5390, 1724, 313),
     (1, 0, 0, 70, 288, 100), (1, 1, 0, 70, 276, 100), (1, 0, 0, 50, 1520, 99), (1, 1, 0, 50, 1454, 99),
     (1, 1, 0, 915, 344, 1259), (1, 0, 0, 129, 274, 5668), (1, 0, 0, 67, 1864, 8208), (1, 1, 0, 8209, 1961, 68),
     (1, 0, 0, 1147, 280, 3651), (1, 1, 0, 8531, 287, 396), (1, 0, 0, 2432, 2112, 3352), (1, 0, 0, 3345, 1618, 2431),
     (1, 0, 0, 7065, 280, 1216), (1, 0, 0, 2919, 271, 2905), (1, 0, 0, 4258, 752, 4032), (1, 1, 0, 2560, 415, 6617),
     (1, 1, 0, 2816, 8448, 711), (1, 1, 0, 8738, 8023, 133),
-    (1, 0, 5, 300, 328, 130), (1, 1, 5, 300, 335, 131), (1, 1, 49, 6912, 288, 960), (1, 0, 1, 3409, 292, 2446),
+    (1, 0, 5, 300, 328, 130), (1, 1, 5, 300, 335, 131), (1, 1, 49, 6912, 288, 960), (1, 0, 9, 2300, 292, 3333),
     (2, 0, 0, 310, 80, 100), (2, 1, 0, 275, 81, 100), (2, 1, 0, 1805, 72, 66), (2, 1, 0, 1984, 66, 8303),
     (2, 0, 0, 321, 144, 5917), (2, 0, 0, 285, 325, 2700), (2, 1, 0, 1864, 8200, 66), (2, 1, 0, 4677, 193, 1458),
     (2, 1, 0, 273, 2000, 2137), (2, 1, 0, 273, 3253, 1285), (2, 1, 0, 2880, 1088, 7433), (2, 1, 0, 1387, 7241, 1078),
