@@ -337,8 +337,15 @@ __device__ __forceinline__ void forward_tile(const MmParams& p, const Work& w, c
   finish_tile<FR, T, TQ, 2, G, NW, G * D * OPB>(acc, p, w.o, w.at, group, tid, s_p, s_q);
 }
 
-// A workgroup per tile.  An expert's last row tile that has at most half its
-// rows takes about half the time.
+// A workgroup per tile.  An expert's last row tile of at most 128 rows is computed
+// as one of 128: 64 experts of 128 rows, 2816 x 2048, 107 -> 89 us.
+//
+// Bound by the matrix cores where there are many rows: 8192^3 takes 381 us (2.9
+// PFLOP/s), 4096 x 18944 x 3584 takes 224 (2.5), 63 % busy at 2.1 GHz, in 4.6
+// rounds of tiles of 256, each with 11 us before its first and behind its last
+// stage.  128-wide tiles read LDS twice as often per product (0.91 us a stage of
+// two tiles against 1.39 of one with four times their size), and start and end
+// under each other.
 template <int KIND, bool GROUPED, int T, int G, int NW>
 __global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) forward_kernel(const MmParams p) {
   __shared__ __attribute__((aligned(1024))) char s_p[G * D * T * SB];
@@ -389,7 +396,8 @@ __global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) forwa
 // Few rows of x, 16 QB of them against 16 rows of w: a workgroup's W waves take
 // every W-th block of 128 of K, straight from memory into MFMA fragments (a
 // row of w is read once; x comes from the caches), and the partial tiles are
-// added through LDS.  Bound by the read of w.  blockIdx.y: which rows of x.
+// added through LDS.  Bound by the read of w: 18944 x 3584 in 13.2 us for one
+// row, 5.1 TB/s.  blockIdx.y: which rows of x.
 template <bool GROUPED, int QB, int W>
 __global__ void __launch_bounds__(64 * W) few_kernel(const MmParams p) {
   __shared__ f32x4 s_part[W - 1][QB][64];

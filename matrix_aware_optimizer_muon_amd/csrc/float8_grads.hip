@@ -303,8 +303,13 @@ __device__ __forceinline__ void mm_tile(const MmParams& p, const Work& w, char* 
   finish_tile<16, T, TQ, WP, G, NW, G * D * OPB>(acc, p, w.o, w.at, group, tid, s_p, s_q);
 }
 
-// A workgroup per tile.  An expert's last row tile that has at most half its
-// rows takes about half the time.
+// A workgroup per tile.  An expert's last row tile of at most 128 rows is computed
+// as one of 128: the input gradient of 61 experts of 128 rows, 1408 x 2048, 87 ->
+// 60 us.
+//
+// A 256-wide stage takes 0.79 us, of which its MFMAs are 0.43 at 2.4 GHz and the
+// reads and writes of LDS as much: 8192 x 3584 x 3584 (weight gradient) 187 us,
+// matrix cores 61 % busy on the 196 units that have a tile.
 template <int KIND, bool GROUPED, int T, int G, int NW>
 __global__ void __launch_bounds__(64 * NW * G, T == 128 && G == 1 ? 2 : 1) mm_kernel(const MmParams p) {
   // (two objects: the compiler then knows that a write to one is no write to

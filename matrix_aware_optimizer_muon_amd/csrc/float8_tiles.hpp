@@ -23,7 +23,8 @@ __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_floa
 // Direct loads into LDS go through a buffer descriptor: 32-bit places from a base
 // that the whole workgroup shares, zeros for a place past the end.  (Beside the
 // global form the compiler can count neither the loads of registers nor the reads
-// of LDS, and waits for all that are out: a gradient's stage took 0.72 us.)
+// of LDS, and waits for all that are out: with the waits of the kernel's own the same, the
+// weight gradient of 8192 x 3584 x 3584 took 195 us instead of 187.)
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 constexpr uint32_t kPast = 0xfffffff0u;
 __device__ __forceinline__ Rsrc rsrc(const char* base) {
