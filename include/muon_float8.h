@@ -45,9 +45,9 @@
  *     between calls are irrelevant.  Results do not depend on timing.
  *   - Outputs may not overlap inputs.
  *   - Errors as in muon.h: host validation first, nothing enqueued on any
- *     status other than MUON_OK and MUON_ERR_HIP.  Dimensions above 2^24, a
- *     product's 8-bit rows more than 2^24 apart and more than 1024 experts give
- *     MUON_ERR_UNSUPPORTED.
+ *     status other than MUON_OK and MUON_ERR_HIP.  Dimensions above 2^24,
+ *     several rows of dy of more than 2^23 columns, a product's 8-bit rows more
+ *     than 2^23 apart and more than 1024 experts give MUON_ERR_UNSUPPORTED.
  */
 #ifndef MUON_FLOAT8_H
 #define MUON_FLOAT8_H

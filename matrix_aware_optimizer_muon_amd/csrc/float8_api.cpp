@@ -32,8 +32,9 @@ bool matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t size)
 constexpr int64_t kFar = 1ll << 36;
 bool far(int64_t ld, int64_t rows) { return rows > 1 && (ld > kFar || ld < -kFar); }
 // 8-bit rows: each starts at a multiple of 16 bytes.  (Kernels add up a tile's
-// row distances in 32 bits: kMaxLd, bytes.)
-constexpr int64_t kMaxLd = 1ll << 24;
+// row distances, and in the forward product K, in 32 bits: kMaxLd, bytes.  dy's
+// that lie further apart are laid out again.)
+constexpr int64_t kMaxLd = 1ll << 23, kMaxGap = 1ll << 24;
 bool matrix8(const void* p, int64_t ld, int64_t rows, int64_t cols) {
   return p && aligned(p, 16) && (rows <= 1 || (ld >= cols && ld % 16 == 0));
 }
@@ -173,7 +174,7 @@ Choice choose(muon_f8_product product, const void* a, int64_t lda, bool grouped,
   if (!fwd && t * n > 0) {
     // bf16 rows that the DMA cannot read: not at 16 bytes, with a last chunk that
     // would leave the matrix, or too far apart
-    c.pack = !aligned(a, 16) || c.lda % 16 || a_cols % 8 || c.lda > kMaxLd;
+    c.pack = !aligned(a, 16) || c.lda % 16 || a_cols % 8 || c.lda > kMaxGap;
     if (c.pack) {
       c.lda = up(a_cols * 2, 16);
       c.bytes = up(t * c.lda, 256);
@@ -195,6 +196,7 @@ muon_status product_sizes(muon_f8_product product, bool grouped, int64_t experts
   if (product < MUON_F8_MATMUL || product > MUON_F8_GRAD_WEIGHT) return MUON_ERR_INVALID_ARGUMENT;
   if (t < 0 || n < 0 || k < 0 || experts < 1 || (!grouped && experts != 1)) return MUON_ERR_INVALID_ARGUMENT;
   if (t > kMaxDim || n > kMaxDim || k > kMaxDim || experts > kMaxExperts) return MUON_ERR_UNSUPPORTED;
+  if (product != MUON_F8_MATMUL && t > 1 && n * 2 > kMaxGap) return MUON_ERR_UNSUPPORTED;
   return MUON_OK;
 }
 

@@ -45,7 +45,7 @@ struct RowOperand {
 #pragma unroll
     for (int i = 0; i < NDMA; ++i) {
       const int r = (wave * NDMA + i) * 8 + lane / 8;
-      // (a row distance is at most 2^24)
+      // (a row distance is at most 2^23, and with it K)
       off[i] = (uint32_t)min(r, count - 1 - row0) * (uint32_t)ld + (((lane & 7) ^ swz_s(r)) << 4);
     }
   }

@@ -76,6 +76,11 @@ def test_product_refusals(kind, kw, want):
 def test_product_refusals_by_kind():
     assert product(0, lda=72) == INVALID                     # 8-bit rows off 16 bytes
     assert product(0, sa=0) == INVALID
+    for kind in (0, 1, 2):                                   # 8-bit rows that 32 bits do not reach
+        assert product(kind, ldb=(1 << 23) + 16) == UNSUPPORTED
+    assert product(0, lda=(1 << 23) + 16) == UNSUPPORTED
+    for kind in (1, 2):
+        assert product(kind, n=(1 << 23) + 8) == UNSUPPORTED
     for kind in (0, 1):                                      # the experts' weights overlap, or lie off 16 bytes
         assert product(kind, ends=P, experts=2, bs=48 * 64 - 16) == INVALID
         assert product(kind, ends=P, experts=2, bs=48 * 64 + 8) == INVALID

@@ -84,6 +84,16 @@ def test_rows_of_a_gradient_far_apart():
     assert torch.equal(f8.grad_weight(far, x), f8.grad_weight(dy, x))
 
 
+def test_8_bit_rows_far_apart():
+    t, n, k, ld = 260, 300, 200, 1 << 23
+    x, w, dy = exact8((t, k), 1, False), exact8((n, k), 2, True), exact_grad((t, n), 3)
+    q = torch.empty(t * ld, dtype=torch.uint8, device="cuda").as_strided((t, k), (ld, 1))
+    q.copy_(x.q.view(torch.uint8))
+    far = f8.F8(q.view(x.q.dtype), x.scale)
+    assert torch.equal(f8.matmul(far, w), f8.matmul(x, w))
+    assert torch.equal(f8.grad_weight(dy, far), f8.grad_weight(dy, x))
+
+
 def test_more_matrices_than_a_launch_has_workgroups():
     """2^24 workgroups and more: the call is cut in parts."""
     x = torch.randn(1000, 1030, device="cuda").bfloat16()
