@@ -6,10 +6,12 @@
  *   out  = g * (max_norm / norm) where norm > max_norm, else g
  *
  * The sum is held in 64 bits, so that no square overflows or vanishes, in a
- * fixed order: the same bits on every run.  The norm is rounded to fp32 once;
- * the factor follows from the 64-bit norm and is rounded to fp32 once, and a
- * product with it to the output's type once.  An infinite norm gives the
- * factor 0 (finite gradients become 0, infinite ones NaN), a NaN one NaN.
+ * fixed order: the same bits on every run.  The norm is rounded to fp32 once
+ * (to infinity past its range); the factor follows from the 64-bit norm and is
+ * rounded once to fp32's 24 bits, also where it is smaller than fp32's normal
+ * numbers; a product with it is rounded to fp32, and from there to the output's
+ * type.  An infinite gradient gives the factor 0 (finite gradients become 0,
+ * infinite ones NaN), a NaN one NaN.
  *
  * Conventions:
  *   - Tensors are flat runs of elements, fp32 or bf16 each (dtypes), aligned to

@@ -9,9 +9,10 @@ global norm over many tensors, and their scaling to a largest norm.
 
 norm = sqrt(sum of all squares), a 0-dim fp32 tensor on the device; no call waits
 for the GPU.  Where norm > max_norm each gradient is multiplied by max_norm /
-norm (in fp32, rounded to the output's type).  An infinite norm makes finite
-gradients 0 and infinite ones NaN, a NaN one all NaN.  Sums are held in 64 bits
-in a fixed order.
+norm (in fp32, rounded to the output's type).  Sums and the norm behind the factor
+are held in 64 bits, in a fixed order: finite gradients are clipped right where
+the norm is infinite in fp32.  An infinite gradient makes finite ones 0 and
+infinite ones NaN, a NaN one all NaN.
 
 Gradients are fp32 or bf16 CUDA tensors of one device, dense (without gaps, in
 any order of dimensions).  Outputs have their gradient's shape and strides and

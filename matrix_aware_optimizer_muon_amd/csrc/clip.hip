@@ -42,15 +42,23 @@ __device__ __forceinline__ double group_sum(double v) {
   return v;
 }
 
-// The factor that takes a norm to at most max_norm.
+// The factor by * 2^exp that takes a norm to at most max_norm.  exp is 0 unless
+// the factor lies under fp32's normal numbers (a norm of 2^126 max_norm and more),
+// where fp32 alone would hold few of its bits; by is then in [1/2, 1].
 struct Factor {
   bool kept;
   float by;
+  int exp;
 };
 __device__ __forceinline__ Factor factor(double norm, float max_norm) {
   const bool kept = norm <= (double)max_norm;
-  return {kept, kept ? 1.0f : (float)((double)max_norm / norm)};
+  double by = kept ? 1.0 : (double)max_norm / norm;
+  int exp = 0;
+  if (by > 0.0 && by < 0x1p-126) by = frexp(by, &exp);
+  return {kept, (float)by, exp};
 }
+// (a product under fp32's normal numbers is rounded once more, and vanishes if exp is not 0)
+__device__ __forceinline__ float times(float v, const Factor& f) { return __builtin_amdgcn_ldexpf(v * f.by, f.exp); }
 
 // The tensor that workgroup b belongs to.
 __device__ __forceinline__ int find(const Table& t, uint32_t b) {
@@ -138,12 +146,12 @@ __global__ void __launch_bounds__(NT) norm_kernel(const double* part, int64_t co
 }
 
 template <typename E, typename O>
-__device__ __forceinline__ void scale(const E* g, O* out, int64_t n, uint32_t j, uint32_t groups, float by) {
+__device__ __forceinline__ void scale(const E* g, O* out, int64_t n, uint32_t j, uint32_t groups, const Factor& f) {
   constexpr int PV = 16 / sizeof(E);
   each<true>(g, n, j, groups, [&](int64_t i, const E* e, int m) {
     O o[PV];
 #pragma unroll
-    for (int l = 0; l < PV; ++l) o[l] = narrow<O>(wide<E>(e[l]) * by);
+    for (int l = 0; l < PV; ++l) o[l] = narrow<O>(times(wide<E>(e[l]), f));
     if (m == PV) {
       // (past the caches, which hold what the first pass read last)
       constexpr int WB = sizeof(O) * PV < 16 ? 8 : 16, NW = sizeof(O) * PV / WB;
@@ -171,12 +179,12 @@ __global__ void __launch_bounds__(NT) scale_kernel(const Table t, const double* 
   const uint32_t j = b - x.first, groups = (uint32_t)((x.n + t.chunk - 1) / t.chunk);
   if (x.gbf16) {
     const uint16_t* g = (const uint16_t*)x.g;
-    if (x.obf16) scale(g, (uint16_t*)x.out, x.n, j, groups, f.by);
-    else scale(g, (float*)x.out, x.n, j, groups, f.by);
+    if (x.obf16) scale(g, (uint16_t*)x.out, x.n, j, groups, f);
+    else scale(g, (float*)x.out, x.n, j, groups, f);
   } else {
     const float* g = (const float*)x.g;
-    if (x.obf16) scale(g, (uint16_t*)x.out, x.n, j, groups, f.by);
-    else scale(g, (float*)x.out, x.n, j, groups, f.by);
+    if (x.obf16) scale(g, (uint16_t*)x.out, x.n, j, groups, f);
+    else scale(g, (float*)x.out, x.n, j, groups, f);
   }
 }
 
@@ -207,12 +215,12 @@ __device__ __forceinline__ void wave_each(const E* g, int n, F f) {
   }
 }
 template <typename E, typename O>
-__device__ __forceinline__ void wave_scale(const E* g, O* out, int n, float by) {
+__device__ __forceinline__ void wave_scale(const E* g, O* out, int n, const Factor& f) {
   constexpr int PV = 16 / sizeof(E);
   wave_each(g, n, [&](int i, const E* e, int m) {
     O o[PV];
 #pragma unroll
-    for (int l = 0; l < PV; ++l) o[l] = narrow<O>(wide<E>(e[l]) * by);
+    for (int l = 0; l < PV; ++l) o[l] = narrow<O>(times(wide<E>(e[l]), f));
     if (m == PV) {
       __builtin_memcpy(out + i, o, sizeof(o));
     } else {
@@ -250,12 +258,12 @@ __global__ void __launch_bounds__(64 * kSmallWaves) small_kernel(const Table t, 
   if (f.kept && x.g == x.out) return;
   if (x.gbf16) {
     const uint16_t* g = (const uint16_t*)x.g + at;
-    if (x.obf16) wave_scale(g, (uint16_t*)x.out + at, n, f.by);
-    else wave_scale(g, (float*)x.out + at, n, f.by);
+    if (x.obf16) wave_scale(g, (uint16_t*)x.out + at, n, f);
+    else wave_scale(g, (float*)x.out + at, n, f);
   } else {
     const float* g = (const float*)x.g + at;
-    if (x.obf16) wave_scale(g, (uint16_t*)x.out + at, n, f.by);
-    else wave_scale(g, (float*)x.out + at, n, f.by);
+    if (x.obf16) wave_scale(g, (uint16_t*)x.out + at, n, f);
+    else wave_scale(g, (float*)x.out + at, n, f);
   }
 }
 
