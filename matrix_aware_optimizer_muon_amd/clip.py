@@ -47,6 +47,7 @@ def grad_norm(grads: Sequence[torch.Tensor]) -> torch.Tensor:
 
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float,
                    out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
-    """Scales the gradients to a global norm of at most max_norm, in place or
-    into `out`, and returns the norm they had (muon_clip_grads)."""
+    """Scales the gradients to a global norm of at most max_norm (a number that
+    fp32 holds, or infinity), in place or into `out`, and returns the norm they
+    had (muon_clip_grads)."""
     return _clip.clip_grad_norm(grads, max_norm, out)

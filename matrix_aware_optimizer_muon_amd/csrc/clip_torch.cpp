@@ -4,6 +4,7 @@
 #include "binding.hpp"
 #include "muon_clip.h"
 
+#include <cmath>
 #include <vector>
 
 namespace {
@@ -78,10 +79,11 @@ PyObject* do_grad_norm(PyObject* const* a, Py_ssize_t n) {
 // grads, max_norm, out or None
 PyObject* do_clip(PyObject* const* a, Py_ssize_t n) {
   count(n, 3);
-  const Tensors g = tensors(a[0], "grads", "a gradient");
   const double max_norm = PyFloat_AsDouble(a[1]);
   if (max_norm == -1.0 && PyErr_Occurred()) throw Raised();
   if (!(max_norm >= 0.0)) bad("max_norm must not be negative");
+  if (std::isinf((float)max_norm) && !std::isinf(max_norm)) bad("max_norm must be infinite or in fp32's range");
+  const Tensors g = tensors(a[0], "grads", "a gradient");
   Tensors made;
   const bool in_place = a[2] == Py_None;
   if (!in_place) {
