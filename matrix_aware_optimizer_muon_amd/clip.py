@@ -19,7 +19,7 @@ any order of dimensions).  Outputs have their gradient's shape and strides and
 either type.  No tensor that is written may share memory with another of the
 call (the same gradient twice included).  Work is enqueued on the current stream
 of the tensors' device.  Argument errors raise ValueError, or MuonError from the
-C ABI.
+C ABI; a forward-mode tangent raises NotImplementedError.
 """
 from __future__ import annotations
 

@@ -101,12 +101,19 @@ at::Tensor make(at::IntArrayRef size, at::ScalarType t, const at::Tensor& like) 
 }
 at::IntArrayRef leading(const at::Tensor& t) { return t.sizes().slice(0, t.dim() - 1); }
 
+// Forward mode is not implemented: a tangent, which no result would carry, raises.
+template <typename... In> void no_tangents(const char* name, const In&... in) {
+  const bool any = (... || (in.defined() && in.unsafeGetTensorImpl()->_fw_grad(/*level=*/0, in).defined()));
+  TORCH_CHECK_NOT_IMPLEMENTED(!any, "forward-mode derivative for ", name, " is not implemented");
+}
+
 // What a forward operator leaves for autograd, if it records and an input
 // requires a gradient: a node that raises when a backward pass reaches it.  Of
 // 8-bit rows the scale carries it.  (The backward operators leave nothing:
-// their results are gradients already.)
+// their results are gradients already; they only refuse tangents.)
 template <typename... In> std::shared_ptr<torch::autograd::Node> undifferentiated(const char* name, const In&... in) {
   using namespace torch::autograd;
+  no_tangents(name, in...);
   if (!compute_requires_grad(in...)) return nullptr;
   return std::shared_ptr<Node>(new NotImplemented(name, collect_next_edges(in...)), deleteNode);
 }

@@ -52,6 +52,7 @@ at::Tensor scratch(const Tensors& g, size_t* need) {
 
 std::shared_ptr<torch::autograd::Node> not_recorded(const char* name, const std::vector<at::Tensor>& in) {
   using namespace torch::autograd;
+  for (const at::Tensor& t : in) no_tangents(name, t);
   bool any = false;
   for (const at::Tensor& t : in) any = any || t.requires_grad();
   if (!any || !c10::GradMode::is_enabled()) return nullptr;
@@ -100,6 +101,7 @@ PyObject* do_clip(PyObject* const* a, Py_ssize_t n) {
     for (size_t i = 0; i < g.t.size(); ++i)
       if (g.t[i].requires_grad() || out.t[i].requires_grad())
         bad("clipping records nothing for autograd: call it without gradients that require one, or under no_grad");
+  for (size_t i = 0; i < g.t.size(); ++i) no_tangents("clip.clip_grad_norm", g.t[i], out.t[i]);
   const c10::DeviceGuard guard(g.t[0].device());
   at::Tensor norm = make({}, at::kFloat, g.t[0]);
   size_t need;

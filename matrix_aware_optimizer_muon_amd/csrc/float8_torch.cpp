@@ -269,6 +269,7 @@ PyObject* do_grad_input(PyObject* const* a, Py_ssize_t n) {
   device(dy);
   device(dy, w.q);
   device(dy, w.scale);
+  no_tangents("float8.grad_input", dy, w.q, w.scale);
   const Ends e = ends_of(a[2], dy);
   const Stack m = weights_of(w, e);
   if (m.r != s.c) bad("w must be (n, k) with dy's last dimension n");
@@ -307,6 +308,7 @@ PyObject* do_grad_weight(PyObject* const* a, Py_ssize_t n) {
   }
   const at::ScalarType st = out.defined() ? out.scalar_type() : dtype(a[3]);
   const muon_dtype t = typed(st, out.defined() ? "out" : "dtype");
+  no_tangents("float8.grad_weight", dy, x.q, x.scale, out);
   const c10::DeviceGuard guard(dy.device());
   if (!out.defined()) out = e.at ? make({e.experts, s.c, r.c}, st, dy) : make({s.c, r.c}, st, dy);
   const Stack o = stack(out, "out", true);

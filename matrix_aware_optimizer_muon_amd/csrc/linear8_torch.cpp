@@ -164,6 +164,7 @@ PyObject* do_rmsnorm_backward(PyObject* const* a, Py_ssize_t n) {
     if (v) device(dy, *v);
   device(dy, rstd);
   device(dy, w);
+  no_tangents("linear8.rmsnorm_backward", dy, *on[0], rstd, w, on[2] ? *on[2] : dy);
   const c10::DeviceGuard guard(dy.device());
   size_t need = 0;
   check(muon_rmsnorm_backward_workspace(s.r, s.c, &need), "muon_rmsnorm_backward_workspace");
@@ -229,6 +230,7 @@ PyObject* do_grad_input(PyObject* const* a, Py_ssize_t n) {
   device(dy);
   device(dy, w.q);
   device(dy, w.scale);
+  no_tangents("linear8.grad_input", dy, w.scale);
   const c10::DeviceGuard guard(dy.device());
   at::Tensor dx = make(shaped(dy, w.s.c), st, dy);
   size_t need;
@@ -261,6 +263,7 @@ PyObject* do_grad_weight(PyObject* const* a, Py_ssize_t n) {
   device(dy, x.q);
   device(dy, x.scale);
   if (out.defined()) device(dy, out);
+  no_tangents("linear8.grad_weight", dy, x.scale, out);
   const c10::DeviceGuard guard(dy.device());
   if (!out.defined()) out = make({s.c, x.s.c}, st, dy);
   const int64_t ldo = rows(out, "out").ld;

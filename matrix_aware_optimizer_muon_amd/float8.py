@@ -30,10 +30,10 @@ Tensors are CUDA tensors with unit stride in the last dimension; dy is bf16, 2-D
 with any row stride or contiguous.  Forward and backward are calls of their own:
 nothing is recorded for autograd.  Where an input of a forward call requires a
 gradient, the result does too, and torch's backward pass through it raises; a
-torch.autograd.Function around the calls gives them a gradient.  Work is
-enqueued on the current stream of the tensors' device; results and workspaces
-come from torch's allocator.  Argument errors raise ValueError, or MuonError from
-the C ABI.
+torch.autograd.Function around the calls gives them a gradient.  A forward-mode
+tangent raises NotImplementedError.  Work is enqueued on the current stream of the
+tensors' device; results and workspaces come from torch's allocator.  Argument
+errors raise ValueError, or MuonError from the C ABI.
 
 The functions only forward to the compiled binding (csrc/float8_torch.cpp),
 which checks, allocates and calls libmuon.so; there is no fallback.
