@@ -293,6 +293,8 @@ PyObject* do_grad_weight(PyObject* const* a, Py_ssize_t n) {
   if (r.r != s.r) bad("dy and x must have the same number of rows");
   const int accumulate = PyObject_IsTrue(a[5]);
   if (accumulate < 0) throw Raised();
+  if (a[4] != Py_None && c10::GradMode::is_enabled() && tensor(a[4], "out").requires_grad())
+    bad("grad_weight records nothing for autograd: out must not require a gradient, or be written under no_grad");
   device(dy);
   device(dy, x.q);
   device(dy, x.scale);

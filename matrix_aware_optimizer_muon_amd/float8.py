@@ -103,6 +103,6 @@ def grad_weight(dy: torch.Tensor, x: F8, ends: Optional[torch.Tensor] = None,
                 dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
                 accumulate: bool = False) -> torch.Tensor:
     """dW = dy^T x (n, k) for bf16 dy (..., n) and rows x (..., k), as `dtype` or
-    into `out`; with ends, (experts, n, k).  accumulate adds to what out holds
-    (muon_f8_grad_weight)."""
+    into `out`, which must not require a gradient (but under no_grad); with ends,
+    (experts, n, k).  accumulate adds to what out holds (muon_f8_grad_weight)."""
     return _float8.grad_weight(dy, x, ends, dtype, out, accumulate)
