@@ -16,7 +16,12 @@
  * significand, subnormals under 2^-6; nearest, ties to even).  Scales are held
  * as e + 127 in a byte (e8m0), 255 for NaN.  A block that holds a NaN or an
  * infinity gets scale NaN and q NaN: what is computed from it is NaN.  Products
- * accept any e4m3 values and any such scales.
+ * accept any e4m3 values and any such scales.  The 8-bit matrix cores (see
+ * muon_f8_matmul) take q and the scale apart; all other products take q * scale
+ * as bf16, the value that muon_f8_dequantize gives: the same under scales from
+ * 2^-124 to 2^119, else rounded to a multiple of 2^-133, or infinite from 2^128
+ * on.  (muon_f8_quantize makes such scales of blocks whose largest magnitude is at
+ * most 448 * 2^-125, 1.1e-35, or over 448 * 2^119, 3.0e38.)
  *
  * Conventions:
  *   - Matrices are row-major with unit column stride; ld* is the distance of
@@ -81,7 +86,8 @@ muon_status muon_f8_workspace(muon_f8_product product, const void* a, int64_t ld
                               int64_t t, int64_t n, int64_t k, muon_dtype dtype, size_t* workspace_bytes);
 
 /* y[t][n] = sum_k (xq[t][k] * x_scale) * (wq[n][k] * w_scale).  An fp32 result,
- * and one of few rows, is summed in fp32 of exact products.  A bf16 result may
+ * and one of few rows, is summed in fp32 of exact products of bf16 operands (see
+ * above).  A bf16 result may
  * be summed by the 8-bit matrix cores, which take eight products at a time and
  * cut each below 2^-13 of the power of two under the largest: an error of at
  * most 2^-10 of the sum of the products' magnitudes, 2^-16 of the result's root

@@ -6,8 +6,8 @@
 // with P on its A side, so each lane ends with four consecutive columns.
 //
 // P's e4m3 values are widened to bf16 with their scale on the way from memory
-// through registers into LDS: exact (4 significant bits, powers of two), two
-// values per instruction, once per workgroup.  Q comes by direct global->LDS
+// through registers into LDS: exact (4 significant bits, powers of two) but at the
+// ends of bf16's range, two values per instruction, once per workgroup.  Q comes by direct global->LDS
 // loads.  Tiles, ring and schedule are those of the 8-bit integer layer's
 // gradients (64 bytes of K per stage, four stages deep, one barrier per stage).
 //

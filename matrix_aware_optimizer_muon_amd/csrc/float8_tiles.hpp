@@ -40,8 +40,10 @@ __device__ __forceinline__ void dma16(Rsrc r, char* to, uint32_t at, uint32_t st
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t*)(uintptr_t)lds, 16, (int)at, (int)step, 0, 0);
 }
 
-// Four e4m3 values times a scale, as bf16: exact, two per instruction.  (A
-// scale's sign and fraction are not looked at; scale 2^-127 included.)
+// Four e4m3 values times a scale, as bf16, two per instruction: exact under scales
+// from 2^-124 to 2^119; else rounded (nearest even) to bf16's subnormals, multiples
+// of 2^-133, or infinite.  (A scale's sign and fraction are not looked at: 0 bits
+// of exponent are 2^-127.)
 __device__ __forceinline__ uint2 widen4(uint32_t v, float scale) {
   return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, scale, false)),
                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, scale, true)));

@@ -19,7 +19,9 @@ An 8-bit tensor is an `F8`: float8_e4m3fn values and float8_e8m0fnu scales
 (value = q * scale), of which a row has one for each 128 columns and a weight
 matrix one for each 128 x 128.  Rows of q start at multiples of 16 bytes: where
 the last dimension is no multiple of 16, `quantize` leaves a gap behind each row,
-and a `.contiguous()` copy of it is refused.
+and a `.contiguous()` copy of it is refused.  Products that do not run on the 8-bit
+matrix cores take q * scale as bf16, as `dequantize` gives it: scales under 2^-124
+lose what lies under 2^-133, and values from 2^128 on are infinite.
 
 Grouped: nothing is copied to the host, so a call can be captured into a graph
 and replayed with other ends.  Experts without rows are allowed.  Rows from the
