@@ -90,7 +90,8 @@ def matmul(x: F8, w: F8, ends: Optional[torch.Tensor] = None,
     w is (experts, n, k) (muon_f8_matmul).  fp32 results are fp32 sums of exact
     products; bf16 ones may come from the 8-bit matrix cores, whose sums inside
     eight products lie up to 2^-10 of their magnitudes off, 2^-16 of the
-    result's root mean square for normally distributed operands."""
+    result's root mean square for normally distributed operands, 2^-15 where
+    some columns of x are far larger than others."""
     return _float8.matmul(x, w, ends, dtype)
 
 
