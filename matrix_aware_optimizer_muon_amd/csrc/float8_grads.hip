@@ -33,13 +33,12 @@ template <bool SQUARE, int T, int NT>
 struct WideOperand {
   static constexpr int CH = T == 64 ? 8 : 16;
   static constexpr int CPR = T / CH;
-  static constexpr int N = KROWS * CPR / NT;  // chunks per lane, KROWS / N rows apart
-  static_assert(N == 1 && KROWS * CPR == NT, "a chunk per lane: two loads that no compiler joins");
-  static constexpr int PC = CH / 4, PIECES = N * PC;
-  static constexpr int LOADS = 2 * N;         // of a stage: values and scale
+  static_assert(KROWS * CPR == NT, "a chunk per lane: two loads that no compiler joins");
+  static constexpr int PIECES = CH / 4;
+  static constexpr int LOADS = 2;  // of a stage: values and scale
   struct Regs {
-    u32x4 v[N];
-    uint32_t scale[N];
+    u32x4 v;
+    uint32_t scale;
   };
   struct Wide {
     uint32_t d[CH / 2];
@@ -64,29 +63,25 @@ struct WideOperand {
   // one is read.
   template <Mode M>
   __device__ __forceinline__ void load(Regs& r, int ks) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      int k = ks * KROWS + row + i * (KROWS / N);
-      if (M != WHOLE) k = min(k, kd - 1);
-      __builtin_memcpy(&r.v[i], src + (int64_t)k * ld, CH);
-      r.scale[i] = scale[(int64_t)(SQUARE ? k / kBlock : k) * lds];
-    }
+    int k = ks * KROWS + row;
+    if (M != WHOLE) k = min(k, kd - 1);
+    __builtin_memcpy(&r.v, src + (int64_t)k * ld, CH);
+    r.scale = scale[(int64_t)(SQUARE ? k / kBlock : k) * lds];
   }
   // Piece q of a stage's way into LDS.
   template <Mode M>
   __device__ __forceinline__ void store(const Regs& r, Wide& w, char* lds_at, int stage, int ks, int q) const {
-    const int i = q / PC, e = q % PC, at_row = row + i * (KROWS / N);
-    const bool past = M != WHOLE && ks * KROWS + at_row >= kd;
-    uint32_t b = past ? 0u : r.v[i][e];
+    const bool past = M != WHOLE && ks * KROWS + row >= kd;
+    uint32_t b = past ? 0u : r.v[q];
     // (opaque: the bytes are taken apart here, not at the load, which would be waited for there)
     asm("" : "+v"(b));
     // (a scale of NaN past the end would make NaN of the zeros)
-    const uint2 d = widen4(b, scale_of(past ? 127u : r.scale[i]));
-    w.d[2 * e] = d.x;
-    w.d[2 * e + 1] = d.y;
-    if (e == PC - 1) {
+    const uint2 d = widen4(b, scale_of(past ? 127u : r.scale));
+    w.d[2 * q] = d.x;
+    w.d[2 * q + 1] = d.y;
+    if (q == PIECES - 1) {
       // swz_k is even, so a lane's two chunks stay side by side
-      const int at = stage + at_row * (T * 2) + ((col * (CH / 8) ^ swz_k<T>(at_row)) << 4);
+      const int at = stage + row * (T * 2) + ((col * (CH / 8) ^ swz_k<T>(row)) << 4);
       *(u32x4*)(lds_at + at) = u32x4{w.d[0], w.d[1], w.d[2], w.d[3]};
       if constexpr (CH == 16) *(u32x4*)(lds_at + at + 16) = u32x4{w.d[4], w.d[5], w.d[6], w.d[7]};
     }

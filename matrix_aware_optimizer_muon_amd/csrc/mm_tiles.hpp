@@ -33,9 +33,6 @@ __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory
 // eight pair places; with 8 chunks (64 columns) row bit 0 is the upper half
 // of the banks already, and bits 1 and 3 make four pair places.
 __device__ __forceinline__ int swz_c(int row) { return ((row >> 2) & 1) << 1; }
-// (reads of 32 rows x 2 chunks: any 16 consecutive rows of one chunk fall on
-// the 16 places of four rows)
-__device__ __forceinline__ int swz_r(int row) { return (row >> 2) & 3; }
 template <int T>
 __device__ __forceinline__ int swz_k(int k) {
   return T == 64 ? ((k >> 1) & 1) << 1 | ((k >> 3) & 1) << 2 : ((k & 3) | (((k >> 3) & 1) << 2)) << 1;
@@ -51,9 +48,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 // One operand of T rows (columns, if K-major) fed by direct global->LDS loads:
 // where a lane's instructions read, stage by stage.  In LDS a stage is 64
-// bytes per row, or 32 rows of 2 T bytes.  Needs 16-byte aligned rows.  ROW32:
-// K-contiguous rows lie as fragments of 32 rows read them.
-template <bool KM, int T, int NW, bool ROW32 = false>
+// bytes per row, or 32 rows of 2 T bytes.  Needs 16-byte aligned rows.
+template <bool KM, int T, int NW>
 struct DmaOperand {
   static constexpr int NDMA = T * KB / 1024 / NW;  // 1-KB instructions per wave and stage
   const char* src[NDMA];   // stage 0
@@ -77,7 +73,7 @@ struct DmaOperand {
         src[i] = base + (int64_t)min(k, kd - 1) * ld + (int64_t)c * 2;
       } else {
         const int r = (wave * NDMA + i) * 16 + (lane >> 2);
-        const int ch = (lane & 3) ^ (ROW32 ? swz_r(r) : swz_c(r));
+        const int ch = (lane & 3) ^ swz_c(r);
         in = full * KB + ch * 16 < kbytes;
         src[i] = base + (int64_t)min(row0 + r, count - 1) * ld + ch * 16;
       }
