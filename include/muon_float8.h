@@ -40,7 +40,9 @@
  *     the last end on belong to none: they are not read, and are set to zero in
  *     y and dx.  Values outside [0, t] count as the nearest of the two, and an
  *     end before its expert's start as no rows; no memory outside the operands
- *     is touched whatever `ends` holds.  ends NULL: all rows belong to the one
+ *     is touched whatever `ends` holds.  (Where ends fall, rows may be claimed by
+ *     two experts: what y and dx then hold is not defined, and dw counts them for
+ *     both.)  ends NULL: all rows belong to the one
  *     matrix (experts must be 1).
  *   - All pointers are device pointers owned by the caller.  A call with no
  *     output elements enqueues nothing and may be given null pointers.

@@ -126,8 +126,11 @@ void choose_dense(Choice& c) {
 // least one (0.45 and 0.75 of 256 rows, of which up to 128 take less time), and
 // no whole rounds: 0.4 of one more than their share.  256-wide ones have to win by
 // 4 %, since fewer tiles spread worse: over 105 sizes, 4 to 4000 rows per expert of
-// uneven numbers, the choice is 1 % off the better one in the mean.  No splits: the
-// tiles of many experts fill the card.
+// uneven numbers, the choice is 1 % off the better one in the mean.  No splits and no
+// wave groups, so the tiles have to fill the card by their number: those of few
+// experts with small matrices and many rows do not (the weight gradients of 2 experts of
+// 16384 rows, 256 x 256, are 8 workgroups and take 285 us; one dense call for
+// each, 15).
 void choose_experts(Choice& c, int64_t experts, int64_t t) {
   const Costs& costs = kCosts[c.kind];
   const bool fwd = c.kind == FWD || c.kind == FWD32;
