@@ -6,7 +6,7 @@
 // factor from them, and scales its chunk.  No atomics, no flags between
 // workgroups: the same bits on every run.
 //
-// Bound by HBM (932 M fp32 elements: 597 us, 6.2 TB/s, and 1372, 5.4): a square
+// Bound by HBM (932 M fp32 elements: 600 us, 6.2 TB/s, and 1377, 5.4): a square
 // costs a conversion and a 64-bit fma, a fraction of its load.  The second pass goes through the tensors backwards, so that what the
 // first read last comes from the last-level cache; where nothing is clipped in
 // place it reads no gradient at all.

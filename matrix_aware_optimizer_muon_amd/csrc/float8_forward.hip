@@ -341,9 +341,9 @@ __device__ __forceinline__ void forward_tile(const MmParams& p, const Work& w, c
 // A workgroup per tile.  An expert's last row tile of at most 128 rows is computed
 // as one of 128: 64 experts of 128 rows, 2816 x 2048, 107 -> 89 us.
 //
-// Bound by the matrix cores where there are many rows: 8192^3 takes 381 us (2.9
-// PFLOP/s), 4096 x 18944 x 3584 takes 224 (2.5), 63 % busy at 2.1 GHz, in 4.6
-// rounds of tiles of 256, each with 11 us before its first and behind its last
+// Bound by the matrix cores where there are many rows: 8192^3 takes 381 to 397 us
+// (2.8 PFLOP/s), 4096 x 18944 x 3584 takes 224 to 241 by card (2.4), 63 % busy at 2.1
+// GHz, in 4.6 rounds of tiles of 256, each with 11 us before its first and behind its last
 // stage.  128-wide tiles read LDS twice as often per product (0.91 us a stage of
 // two tiles against 1.39 of one with four times their size), and start and end
 // under each other.
