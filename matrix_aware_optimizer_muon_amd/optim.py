@@ -7,11 +7,13 @@ t mod K == 0 and the RowNorm step otherwise; K = 0 refreshes every step.
 """
 from __future__ import annotations
 
+import ctypes
+import math
 from typing import List, Optional, Sequence
 
 import torch
 
-from ._lib import Hparams, Plan
+from ._lib import MUON_ERR_INVALID_ARGUMENT, Hparams, MuonError, Plan
 
 
 class MuonMI355X:
@@ -46,10 +48,6 @@ class MuonMI355X:
         global norm of at most that (clip.clip_grad_norm), and the norm they
         had is returned."""
         self._check(grads)
-        norm = None
-        if max_norm is not None:
-            from .clip import clip_grad_norm
-            norm = clip_grad_norm(grads, max_norm)
         if refresh is None:
             refresh = self.refresh_period <= 0 or self.t % self.refresh_period == 0
         stream = torch.cuda.current_stream(self.params[0].device).cuda_stream
@@ -57,6 +55,13 @@ class MuonMI355X:
                 [g.data_ptr() for g in grads], lr, weight_decay, self.workspace.data_ptr(),
                 self.workspace.numel(), stream,
                 [o.data_ptr() for o in out] if out is not None else None)
+        norm = None
+        if max_norm is not None:
+            from .clip import clip_grad_norm
+            # (what the step refuses, ahead of the first write)
+            if not all(math.isfinite(ctypes.c_float(v).value) for v in (lr, weight_decay)):
+                raise MuonError(MUON_ERR_INVALID_ARGUMENT, "step")
+            norm = clip_grad_norm(grads, max_norm)
         if refresh:
             self.plan.step_ptrs(*args)
         else:
